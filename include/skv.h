@@ -64,8 +64,9 @@ enum skv_status {
   SKV_ERR_TABLE = 6,        /* histogram too large for the p_hat table: its smoothed total
                                H(N) = sum over patterns of (hist + 1), an exact integer, has
                                Mp * H(N) > 2^62 (this includes a total beyond 2^64) */
-  SKV_ERR_SCRATCH = 7       /* skv_decode_static: the shape's decode workspace is larger than
+  SKV_ERR_SCRATCH = 7,      /* skv_decode_static: the shape's decode workspace is larger than
                                SKV_STATIC_SCRATCH_BYTES */
+  SKV_ERR_PAGES = 8         /* paged cache: too few free pages, or a sequence longer than its table row */
 };
 
 enum skv_sym_fmt { SKV_SYM_BF16 = 0, SKV_SYM_E4M3 = 1 };
@@ -248,6 +249,173 @@ int skv_decode(const skv_shape *shape, const uint8_t *bits, size_t bits_bytes,
 int skv_decode_static(const skv_shape *shape, const uint8_t *bits, size_t bits_bytes,
                       const uint64_t *offsets, const void *mu, const float *sigma, const uint64_t *hist,
                       void *x_out, int32_t *status, void *stream);
+
+/* ---------------------------------------------------------------- paged cache */
+/*
+ * A KV cache kept in pages, as a serving program holds it between the model
+ * and the coder: many sequences of different lengths in one pool, sequences
+ * that share a prefix sharing its pages, attention that reads the pages in
+ * place, and single sequences read out into the coder's layout and back.
+ *
+ * Arrays (device, the caller's):
+ *   pool   [layers][n_pages][2 (K=0, V=1)][kv_heads][page_tokens][head_dim]
+ *          symbols (bf16 or e4m3 patterns), 16-byte aligned.  A page id names
+ *          the page of that index in every layer.
+ *   table  int32 [max_seqs][max_pages]: row s holds the ids of sequence s's
+ *          pages, token t in entry t / page_tokens; entries behind the last
+ *          page are -1.
+ *   lens   int32 [max_seqs]: tokens of each sequence; 0 = a free row.
+ *   refs   int32 [n_pages], 16-byte aligned: table entries that name the page;
+ *          0 = a free page.
+ *
+ * Lists of sequences (seqs, src, dst) are int32 row numbers on the device; a
+ * negative one is a padded place, which the call passes over.
+ *
+ * Errors.  Unlike the coder's calls, these never clear `*status`: it keeps the
+ * first error of all calls since the caller cleared it, so that one read per
+ * step covers every layer.  A table, a length or an id that does not fit the
+ * arrays is SKV_ERR_ARG; whatever these arrays hold, no kernel leaves them.
+ *
+ * Calls on one cache are ordered by their stream; calls that change a cache
+ * (all but gather and attend) must not overlap with others on it.  Workspaces
+ * need no initialisation, and overlapping calls use distinct ones.  No call
+ * allocates, synchronises or copies to the host: all can be captured in a
+ * graph, which takes the lengths, tables and lists of the moment of replay.
+ */
+typedef struct skv_pages_shape {
+  int64_t layers;      /* >= 1 */
+  int64_t kv_heads;    /* >= 1 */
+  int64_t head_dim;    /* multiple of 8 dividing 512 */
+  int64_t page_tokens; /* 16, 32, 64, 128 or 256: a coder chunk is a whole number of pages */
+  int64_t n_pages;     /* 1 .. 2^30 */
+  int64_t max_seqs;    /* 1 .. 2^20 */
+  int64_t max_pages;   /* entries of a table row; max_pages * page_tokens < 2^31 */
+  int32_t sym_fmt;     /* enum skv_sym_fmt */
+  int32_t reserved;    /* 0 */
+} skv_pages_shape;
+
+typedef struct skv_pages {
+  void *pool;
+  int32_t *table;
+  int32_t *lens;
+  int32_t *refs;
+} skv_pages;
+
+/* Bytes of the pool, and of the workspace that extend, fork, truncate and
+ * compact take (host only). */
+int skv_pages_pool_size(const skv_pages_shape *shape, size_t *bytes);
+int skv_pages_workspace_size(const skv_pages_shape *shape, size_t *bytes);
+
+/* Empty the cache: table -1, lens 0, refs 0.  The pool is left as it is. */
+int skv_pages_reset(const skv_pages_shape *shape, const skv_pages *pages, void *stream);
+
+/*
+ * Make room for n_new[i] >= 0 more tokens of sequence seqs[i], i < n <=
+ * max_seqs: lens grows, new pages are appended to the row.  A sequence that
+ * grows into a last page which others hold too gets a copy of that page first
+ * (its tokens below the length, all layers).  As if in list order: the last of
+ * the sharers keeps the page when no sequence outside the list holds it.  In
+ * list order, a sequence's copy before its new pages, each takes the lowest
+ * page that was free when the call began.  The tokens themselves are unwritten
+ * until skv_pages_store or skv_pages_scatter.
+ *   SKV_ERR_PAGES: not enough free pages, or a row overflows; SKV_ERR_ARG: a
+ *   row out of range or listed twice, n_new < 0, or a broken table.  In both
+ *   cases the cache is unchanged.
+ */
+int skv_pages_extend(const skv_pages_shape *shape, const skv_pages *pages, const int32_t *seqs,
+                     const int32_t *n_new, int64_t n, void *workspace, size_t workspace_bytes,
+                     int32_t *status, void *stream);
+
+/*
+ * Fork: row dst[i] becomes the first n_tokens[i] tokens of row src[i] (all of
+ * them where n_tokens is NULL), holding the same pages; nothing is copied
+ * until one of the holders grows.  src may repeat; every dst is a free row
+ * (length 0), listed once and no src of this call.  A pair is padding where
+ * either is negative.
+ *   SKV_ERR_ARG, cache unchanged: a row that breaks these rules, or n_tokens
+ *   outside [0, length].
+ */
+int skv_pages_fork(const skv_pages_shape *shape, const skv_pages *pages, const int32_t *src,
+                   const int32_t *dst, const int32_t *n_tokens, int64_t n, void *workspace,
+                   size_t workspace_bytes, int32_t *status, void *stream);
+
+/*
+ * Keep the first keep[i] tokens of sequence seqs[i] (none where keep is NULL:
+ * the row is freed).  Pages that no token is left in are given back.
+ *   SKV_ERR_ARG, cache unchanged: a row out of range or listed twice, or
+ *   keep[i] outside [0, length].
+ */
+int skv_pages_truncate(const skv_pages_shape *shape, const skv_pages *pages, const int32_t *seqs,
+                       const int32_t *keep, int64_t n, void *workspace, size_t workspace_bytes,
+                       int32_t *status, void *stream);
+
+/*
+ * Move the pages in use to ids 0 .. *n_live - 1 (n_live: device int32, the
+ * number of pages with refs > 0) and rewrite table and refs: the k-th free
+ * page below n_live takes the k-th used page at or above it, so that the
+ * fewest pages move.  What lies behind is free to be given to another use.
+ */
+int skv_pages_compact(const skv_pages_shape *shape, const skv_pages *pages, int32_t *n_live,
+                      void *workspace, size_t workspace_bytes, int32_t *status, void *stream);
+
+/*
+ * Write keys and values of n tokens into layer `layer`: token i to position
+ * pos[i] of sequence seqs[i], 0 <= pos[i] < its length.
+ *   k, v      (device) bf16 [n][kv_heads][head_dim], rows k_stride, v_stride
+ *             elements apart (multiples of 8, >= kv_heads * head_dim); 16-byte
+ *             aligned
+ *   k_scale, v_scale  (device) fp32 [kv_heads], e4m3 caches only, or NULL (1):
+ *             the symbol is e4m3(x / scale), the quotient rounded to fp32, then
+ *             to nearest even, beyond +-448 held there; NaN stays NaN
+ * A token with a bad row or position, or whose page is held more than once, is
+ * left out with SKV_ERR_ARG.  Each (sequence, position) appears at most once
+ * in a call; of two tokens for one place, which is kept is not specified.
+ */
+int skv_pages_store(const skv_pages_shape *shape, const skv_pages *pages, int64_t layer, const void *k,
+                    int64_t k_stride, const void *v, int64_t v_stride, const float *k_scale,
+                    const float *v_scale, const int32_t *seqs, const int32_t *pos, int64_t n,
+                    int32_t *status, void *stream);
+
+/*
+ * Tokens [first, first + tokens) of row `seq`, all layers, into x (device, the
+ * coder's layout [layers][2][kv_heads][tokens][head_dim], 16-byte aligned), and
+ * back: the cache of one sequence on its way to skv_encode, and from
+ * skv_decode.  SKV_ERR_ARG (status) and nothing written where the row holds
+ * fewer tokens, or, by scatter, into a page that is held more than once.
+ */
+int skv_pages_gather(const skv_pages_shape *shape, const skv_pages *pages, int64_t seq, int64_t first,
+                     int64_t tokens, void *x, int32_t *status, void *stream);
+int skv_pages_scatter(const skv_pages_shape *shape, const skv_pages *pages, int64_t seq, int64_t first,
+                      int64_t tokens, const void *x, int32_t *status, void *stream);
+
+/* Workspace of skv_attend for this cache and number of query heads (host
+ * only); it depends neither on the batch nor on the lengths. */
+int skv_attend_workspace_size(const skv_pages_shape *shape, int64_t q_heads, size_t *bytes);
+
+/*
+ * Attention of one new token per sequence over its cached tokens, in layer
+ * `layer`.  With t over the lens[s] tokens of s = seqs[i] and g = q_heads /
+ * kv_heads query heads to a KV head, for query head j and h = j / g:
+ *   z_t = scale * k_scale[h] * (q_j . k_{h,t})
+ *   lse = log(sum_t exp(z_t)),  out_j = v_scale[h] * sum_t exp(z_t - lse) v_{h,t}
+ * A sequence without tokens has out 0 and lse -inf.  What the pages hold behind
+ * the last token is never used, NaN or not; a padded row's out and lse are left
+ * as they are.
+ *   q       (device) bf16 [n][q_heads][head_dim], rows q_stride elements apart
+ *           (a multiple of 8, >= q_heads * head_dim); 16-byte aligned
+ *   k_scale, v_scale  (device) fp32 [kv_heads], e4m3 caches only, or NULL (1)
+ *   seqs    (device) int32 [n], rows may repeat
+ *   out     (device) bf16 [n][q_heads][head_dim], 16-byte aligned
+ *   lse     (device) fp32 [n][q_heads], or NULL
+ * Scores, softmax statistics and sums are fp32.  The result is the same for
+ * every call with the same inputs on the same GPU model.  SKV_ERR_ARG (status):
+ * a row or page out of range, or a length beyond the table row; that row's
+ * output is then unspecified.
+ */
+int skv_attend(const skv_pages_shape *shape, const skv_pages *pages, int64_t layer, const void *q,
+               int64_t q_stride, int64_t q_heads, float scale, const float *k_scale, const float *v_scale,
+               const int32_t *seqs, int64_t n, void *out, float *lse, void *workspace,
+               size_t workspace_bytes, int32_t *status, void *stream);
 
 /* ---------------------------------------------------------------- kernel timing */
 

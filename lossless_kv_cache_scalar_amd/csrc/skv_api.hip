@@ -18,6 +18,7 @@ extern "C" const char *skv_status_string(int status) {
     case SKV_ERR_CORRUPT: return "corrupt stream";
     case SKV_ERR_TABLE: return "histogram too large for the p_hat table";
     case SKV_ERR_SCRATCH: return "shape needs more than the library's static scratch (skv_decode_static)";
+    case SKV_ERR_PAGES: return "no room in the paged cache (too few free pages, or a table row overflows)";
     default: return "unknown status";
   }
 }

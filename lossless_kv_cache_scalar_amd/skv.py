@@ -7,6 +7,7 @@ entry points raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -15,7 +16,7 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_lib", "libskv.so")
 
-OK, ERR_ARG, ERR_UNSUPPORTED, ERR_HIP, ERR_CAPACITY, ERR_CORRUPT, ERR_TABLE, ERR_SCRATCH = range(8)
+OK, ERR_ARG, ERR_UNSUPPORTED, ERR_HIP, ERR_CAPACITY, ERR_CORRUPT, ERR_TABLE, ERR_SCRATCH, ERR_PAGES = range(9)
 STATIC_SCRATCH_BYTES = 16 << 20  # SKV_STATIC_SCRATCH_BYTES
 SYM_BF16, SYM_E4M3 = 0, 1
 MU_BF16, MU_F32 = 0, 1
@@ -27,14 +28,26 @@ OCT_STRIDE = 1 + OCTAVES
 # every function skv.h declares, in declaration order
 EXPORTS = ["skv_status_string", "skv_num_chunks", "skv_encode_bound", "skv_workspace_size",
            "skv_calib_state_size", "skv_calib_reset", "skv_calib_accumulate", "skv_calib_finalize",
-           "skv_calibrate", "skv_encode", "skv_decode", "skv_decode_static", "skv_timing_start", "skv_timing_stop",
-           "skv_timed_kernel_name"]
+           "skv_calibrate", "skv_encode", "skv_decode", "skv_decode_static", "skv_pages_pool_size",
+           "skv_pages_workspace_size", "skv_pages_reset", "skv_pages_extend", "skv_pages_fork", "skv_pages_truncate",
+           "skv_pages_compact", "skv_pages_store", "skv_pages_gather", "skv_pages_scatter", "skv_attend_workspace_size",
+           "skv_attend", "skv_timing_start", "skv_timing_stop", "skv_timed_kernel_name"]
 
 
 class SkvShape(C.Structure):
     _fields_ = [("layers", C.c_int64), ("kv_heads", C.c_int64), ("tokens", C.c_int64),
                 ("head_dim", C.c_int64), ("sym_fmt", C.c_int32), ("mu_fmt", C.c_int32),
                 ("sigma_mode", C.c_int32), ("phat_mode", C.c_int32)]
+
+
+class SkvPagesShape(C.Structure):
+    _fields_ = [("layers", C.c_int64), ("kv_heads", C.c_int64), ("head_dim", C.c_int64), ("page_tokens", C.c_int64),
+                ("n_pages", C.c_int64), ("max_seqs", C.c_int64), ("max_pages", C.c_int64), ("sym_fmt", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
+class SkvPages(C.Structure):
+    _fields_ = [("pool", C.c_void_p), ("table", C.c_void_p), ("lens", C.c_void_p), ("refs", C.c_void_p)]
 
 
 class SkvError(RuntimeError):
@@ -67,6 +80,19 @@ def load():
     L.skv_encode.argtypes = [sp, vp, vp, vp, vp, vp, sz, vp, vp, sz, i32p, vp]
     L.skv_decode.argtypes = [sp, vp, sz, vp, vp, vp, vp, vp, vp, sz, i32p, vp]
     L.skv_decode_static.argtypes = [sp, vp, sz, vp, vp, vp, vp, vp, i32p, vp]
+    pp, pg = C.POINTER(SkvPagesShape), C.POINTER(SkvPages)
+    for name in ("skv_pages_pool_size", "skv_pages_workspace_size"):
+        getattr(L, name).argtypes = [pp, C.POINTER(C.c_size_t)]
+    L.skv_pages_reset.argtypes = [pp, pg, vp]
+    L.skv_pages_extend.argtypes = [pp, pg, vp, vp, i64, vp, sz, i32p, vp]
+    L.skv_pages_fork.argtypes = [pp, pg, vp, vp, vp, i64, vp, sz, i32p, vp]
+    L.skv_pages_truncate.argtypes = [pp, pg, vp, vp, i64, vp, sz, i32p, vp]
+    L.skv_pages_compact.argtypes = [pp, pg, vp, vp, sz, i32p, vp]
+    L.skv_pages_store.argtypes = [pp, pg, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, i32p, vp]
+    for name in ("skv_pages_gather", "skv_pages_scatter"):
+        getattr(L, name).argtypes = [pp, pg, i64, i64, i64, vp, i32p, vp]
+    L.skv_attend_workspace_size.argtypes = [pp, i64, C.POINTER(C.c_size_t)]
+    L.skv_attend.argtypes = [pp, pg, i64, vp, i64, i64, C.c_float, vp, vp, vp, i64, vp, vp, vp, sz, i32p, vp]
     L.skv_timing_start.argtypes = [C.c_int32]
     L.skv_timing_stop.argtypes = [C.POINTER(C.c_int32), C.POINTER(C.c_float), C.c_int32, C.POINTER(C.c_int32)]
     L.skv_timed_kernel_name.argtypes = [C.c_int32]
@@ -298,3 +324,226 @@ def calibrate_sequences(seq_shape: SkvShape, seqs, device="cuda", stream=None):
         _check(calib_accumulate(state, seq_shape, x, mu, stream), "skv_calib_accumulate")
     _check(calib_finalize(state, seq_shape, sigma, hist, stream), "skv_calib_finalize")
     return sigma, hist
+
+
+# ---- paged cache ----
+def pages_shape(layers, kv_heads, head_dim, page_tokens, n_pages, max_seqs, max_pages, sym_fmt=SYM_BF16) -> SkvPagesShape:
+    return SkvPagesShape(int(layers), int(kv_heads), int(head_dim), int(page_tokens), int(n_pages), int(max_seqs),
+                         int(max_pages), int(sym_fmt), 0)
+
+
+def pages_pool_size(sh: SkvPagesShape) -> int:
+    return _size("skv_pages_pool_size", sh)
+
+
+def pages_workspace_size(sh: SkvPagesShape) -> int:
+    return _size("skv_pages_workspace_size", sh)
+
+
+def attend_workspace_size(sh: SkvPagesShape, q_heads: int) -> int:
+    n = C.c_size_t(0)
+    _check(load().skv_attend_workspace_size(C.byref(sh), int(q_heads), C.byref(n)), "skv_attend_workspace_size")
+    return n.value
+
+
+class Pages:
+    """A paged KV cache and the calls on it (skv.h, "paged cache").
+
+    The arrays may be given (contiguous, of the shape's sizes) or are made here
+    and emptied.  `q_heads` is the number of query heads `attend` will be called
+    with (0: no attend).  Every call enqueues on `stream` or the current one and
+    returns at once; errors that the device finds stay in `status` until
+    `check()` reads and clears them.  Lists are int32 tensors on the cache's
+    device, which has to be the current one.
+    """
+
+    def __init__(self, sh: SkvPagesShape, pool=None, table=None, lens=None, refs=None, q_heads: int = 0, device="cuda"):
+        pool_bytes, ws = pages_pool_size(sh), pages_workspace_size(sh)
+        att = attend_workspace_size(sh, q_heads) if q_heads else 0
+        made = (pool, table, lens, refs)
+        if any(t is None for t in made) and not all(t is None for t in made):
+            raise SkvError("pool, table, lens and refs are given together, or none of them")
+        new = pool is None
+        if new:
+            dt = torch.int16 if sh.sym_fmt == SYM_BF16 else torch.uint8
+            pool = torch.empty(sh.layers, sh.n_pages, 2, sh.kv_heads, sh.page_tokens, sh.head_dim, dtype=dt, device=device)
+            table = torch.empty(sh.max_seqs, sh.max_pages, dtype=torch.int32, device=device)
+            lens = torch.empty(sh.max_seqs, dtype=torch.int32, device=device)
+            refs = torch.empty(sh.n_pages, dtype=torch.int32, device=device)
+        self.shape, self.q_heads = sh, int(q_heads)
+        self.pool, self.table, self.lens, self.refs = pool, table, lens, refs
+        _fits(pool, pool_bytes, "pool")
+        for t, n, what in ((table, sh.max_seqs * sh.max_pages, "table"), (lens, sh.max_seqs, "lens"), (refs, sh.n_pages, "refs")):
+            _int32(t, n, what)
+        self.device = pool.device
+        for t, what in ((pool, "pool"), (table, "table"), (lens, "lens"), (refs, "refs")):
+            self._here(t, what)
+        self.ws_bytes, self.attend_bytes = ws, att
+        self.workspace = torch.empty(ws, dtype=torch.uint8, device=self.device)
+        self.attend_workspace = torch.empty(att, dtype=torch.uint8, device=self.device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._pages = SkvPages(pool.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr())
+        self._sh, self._pg = C.byref(sh), C.byref(self._pages)
+        if new:
+            self.reset()
+        torch.cuda.current_stream().synchronize()  # the arrays are ready for calls on any stream
+
+    def _here(self, t, what: str):
+        if t.device.type != "cuda" or t.device != self.device:
+            raise SkvError(f"{what}: on {t.device}, not on the cache's GPU")
+
+    def _call(self, stream):
+        """The stream of a call, once the cache's device is seen to be the current one."""
+        if torch.cuda.current_device() != self.device.index:
+            raise SkvError(f"the cache is on {self.device}, the current device is cuda:{torch.cuda.current_device()}")
+        return _stream(stream)
+
+    def _made_on(self, stream):
+        """What a call makes itself is made on the call's stream."""
+        if stream is None:
+            return contextlib.nullcontext()
+        return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+    def _list(self, t, n, what: str):
+        n = t.numel() if n is None else n
+        _int32(t, n, what)
+        if t.numel() != n:
+            raise SkvError(f"{what}: {t.numel()} entries, {n} wanted")
+        self._here(t, what)
+        return n
+
+    def _rows(self, t, n, heads, what: str):
+        """A bf16 [n][heads][head_dim] argument whose rows may lie apart; its row stride in elements."""
+        d = self.shape.head_dim
+        if t.dtype != torch.bfloat16 or t.dim() != 3 or tuple(t.shape) != (n, heads, d):
+            raise SkvError(f"{what}: {t.dtype} {list(t.shape)}, bfloat16 {[n, heads, d]} wanted")
+        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+            raise SkvError(f"{what}: heads and channels are not contiguous")
+        self._here(t, what)
+        return t.stride(0) if n > 1 else heads * d
+
+    def _scales(self, t, what: str):
+        if t is None:
+            return None
+        if t.dtype != torch.float32:
+            raise SkvError(f"{what}: {t.dtype}, float32 wanted")
+        _fits(t, 4 * self.shape.kv_heads, what)
+        self._here(t, what)
+        return t.data_ptr()
+
+    def reset(self, stream=None) -> None:
+        """skv_pages_reset: no sequences, every page free."""
+        _check(load().skv_pages_reset(self._sh, self._pg, self._call(stream)), "skv_pages_reset")
+
+    def check(self, stream=None) -> None:
+        """Wait for the stream, then raise the first error that the device found since the last check."""
+        with self._made_on(stream):
+            code = int(self.status.item())
+            if code != OK:
+                self.status.zero_()
+        if code != OK:
+            raise SkvError(f"paged cache: {status_string(code)} ({code})")
+
+    def extend(self, seqs, n_new, stream=None) -> None:
+        """skv_pages_extend: room for n_new[i] more tokens of sequence seqs[i]."""
+        n = self._list(seqs, None, "seqs")
+        self._list(n_new, n, "n_new")
+        _check(load().skv_pages_extend(self._sh, self._pg, seqs.data_ptr(), n_new.data_ptr(), n, self.workspace.data_ptr(),
+                                       self.ws_bytes, self.status.data_ptr(), self._call(stream)), "skv_pages_extend")
+
+    def fork(self, src, dst, n_tokens=None, stream=None) -> None:
+        """skv_pages_fork: row dst[i] shares the pages of row src[i] (of its first n_tokens[i] tokens)."""
+        n = self._list(src, None, "src")
+        self._list(dst, n, "dst")
+        if n_tokens is not None:
+            self._list(n_tokens, n, "n_tokens")
+        _check(load().skv_pages_fork(self._sh, self._pg, src.data_ptr(), dst.data_ptr(), _ptr(n_tokens), n,
+                                     self.workspace.data_ptr(), self.ws_bytes, self.status.data_ptr(),
+                                     self._call(stream)), "skv_pages_fork")
+
+    def truncate(self, seqs, keep=None, stream=None) -> None:
+        """skv_pages_truncate: keep keep[i] tokens of sequence seqs[i]; free the rows without keep."""
+        n = self._list(seqs, None, "seqs")
+        if keep is not None:
+            self._list(keep, n, "keep")
+        _check(load().skv_pages_truncate(self._sh, self._pg, seqs.data_ptr(), _ptr(keep), n, self.workspace.data_ptr(),
+                                         self.ws_bytes, self.status.data_ptr(), self._call(stream)), "skv_pages_truncate")
+
+    def compact(self, n_live=None, stream=None):
+        """skv_pages_compact; the number of pages in use, an int32 tensor of one."""
+        if n_live is None:
+            with self._made_on(stream):
+                n_live = torch.empty(1, dtype=torch.int32, device=self.device)
+        self._list(n_live, 1, "n_live")
+        _check(load().skv_pages_compact(self._sh, self._pg, n_live.data_ptr(), self.workspace.data_ptr(), self.ws_bytes,
+                                        self.status.data_ptr(), self._call(stream)), "skv_pages_compact")
+        return n_live
+
+    def store(self, layer: int, k, v, seqs, pos, k_scale=None, v_scale=None, stream=None) -> None:
+        """skv_pages_store: keys and values [n][kv_heads][head_dim] to positions pos of sequences seqs."""
+        n = self._list(seqs, None, "seqs")
+        self._list(pos, n, "pos")
+        ks = self._rows(k, n, self.shape.kv_heads, "k")
+        vs = self._rows(v, n, self.shape.kv_heads, "v")
+        _check(load().skv_pages_store(self._sh, self._pg, int(layer), k.data_ptr(), ks, v.data_ptr(), vs,
+                                      self._scales(k_scale, "k_scale"), self._scales(v_scale, "v_scale"), seqs.data_ptr(),
+                                      pos.data_ptr(), n, self.status.data_ptr(), self._call(stream)), "skv_pages_store")
+
+    def coder_shape(self, tokens: int, mu_fmt=MU_BF16, sigma_mode=SIGMA_CHANNEL, phat_mode=PHAT_STATIC) -> SkvShape:
+        """The coder's shape of `tokens` tokens of one sequence."""
+        return shape(self.shape.layers, self.shape.kv_heads, tokens, self.shape.head_dim, self.shape.sym_fmt, mu_fmt,
+                     sigma_mode, phat_mode)
+
+    def _tokens(self, tokens, x):
+        sh = self.shape
+        _fits(x, sh.layers * 2 * sh.kv_heads * max(int(tokens), 0) * sh.head_dim * (2 if sh.sym_fmt == SYM_BF16 else 1), "x")
+        self._here(x, "x")
+
+    def gather(self, seq: int, first: int, tokens: int, x=None, stream=None):
+        """skv_pages_gather: tokens [first, first + tokens) of a sequence in the coder's layout, as encode() takes them."""
+        sh = self.shape
+        if x is None:
+            with self._made_on(stream):
+                x = torch.empty(sh.layers, 2, sh.kv_heads, int(tokens), sh.head_dim, device=self.device,
+                                dtype=torch.int16 if sh.sym_fmt == SYM_BF16 else torch.uint8)
+        self._tokens(tokens, x)
+        _check(load().skv_pages_gather(self._sh, self._pg, int(seq), int(first), int(tokens), x.data_ptr(),
+                                       self.status.data_ptr(), self._call(stream)), "skv_pages_gather")
+        return x
+
+    def scatter(self, seq: int, first: int, tokens: int, x, stream=None) -> None:
+        """skv_pages_scatter: the way back, from decode()'s output into the sequence's pages."""
+        self._tokens(tokens, x)
+        _check(load().skv_pages_scatter(self._sh, self._pg, int(seq), int(first), int(tokens), x.data_ptr(),
+                                        self.status.data_ptr(), self._call(stream)), "skv_pages_scatter")
+
+    def attend(self, layer: int, q, seqs, scale=None, k_scale=None, v_scale=None, out=None, lse=None, stream=None):
+        """skv_attend: attention of q [n][q_heads][head_dim], one token of each sequence in seqs, over the cached
+        tokens; scale is 1 / sqrt(head_dim) unless given.  Without `out`, padded rows come back as zeros."""
+        n = self._list(seqs, None, "seqs")
+        if not self.q_heads:
+            raise SkvError("attend: the cache was made without q_heads")
+        qs = self._rows(q, n, self.q_heads, "q")
+        if out is None:
+            with self._made_on(stream):
+                out = torch.zeros(n, self.q_heads, self.shape.head_dim, dtype=torch.bfloat16, device=self.device)
+        elif self._rows(out, n, self.q_heads, "out") != self.q_heads * self.shape.head_dim:
+            raise SkvError("out: not contiguous")
+        if lse is not None:
+            if lse.dtype != torch.float32 or tuple(lse.shape) != (n, self.q_heads):
+                raise SkvError(f"lse: {lse.dtype} {list(lse.shape)}, float32 {[n, self.q_heads]} wanted")
+            _fits(lse, 4 * n * self.q_heads, "lse")
+            self._here(lse, "lse")
+        if scale is None:
+            scale = self.shape.head_dim ** -0.5
+        _check(load().skv_attend(self._sh, self._pg, int(layer), q.data_ptr(), qs, self.q_heads, float(scale),
+                                 self._scales(k_scale, "k_scale"), self._scales(v_scale, "v_scale"), seqs.data_ptr(), n,
+                                 out.data_ptr(), _ptr(lse), self.attend_workspace.data_ptr(), self.attend_bytes,
+                                 self.status.data_ptr(), self._call(stream)), "skv_attend")
+        return out
+
+
+def _int32(t, n: int, what: str):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+        raise SkvError(f"{what}: an int32 tensor is wanted")
+    _fits(t, 4 * n, what)
