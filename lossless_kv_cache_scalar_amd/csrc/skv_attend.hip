@@ -46,8 +46,17 @@ struct AttendArgs {
   int waves;                    // of the main launch
   uint16_t *out;
   float *lse;
-  float *part;                  // [waves][2][kept * (D + 2)]
+  int slot;                     // floats of a partial sum: O [kept][D], m [kept], l [kept], rounded up to 4
+  float *part;                  // [waves][2][slot]
+  int4 *split;                  // [waves] the row that begins in a wave's run and ends in another's (Split)
 };
+
+// what a wave leaves about such a row: waves it spans (0: there is none) and
+// where its first partial sum lies, its first query head's row in out, its
+// heads, its KV head
+__device__ __forceinline__ int4 split_of(int parts, int slot, int32_t qrow, int heads, int h) {
+  return make_int4(parts << 1 | slot, qrow, heads, h);
+}
 
 // ---- the dealing out ----
 // units of list place i; 0 for padding.  An empty sequence has one unit, whose
@@ -282,38 +291,48 @@ __global__ __launch_bounds__(64) void k_attend(PGeo g, skv_pages a, int layer, A
   const int rows_of_place = g.heads * p.tiles_q;
 
   // units in all, and the place that this wave's run begins in
-  int64_t units = 0;
-  bool there, bad;
-  for (int c = 0; c < p.n; c += 64) {
-    const int32_t len = place_len(g, a, p, c + lane, there, bad);
-    const int64_t u = there ? (int64_t)tiles_of(len) * rows_of_place : 0;
-    units += lane_of(wave_scan(u), 63);
-    if (bad && blockIdx.x == 0) set_status(status, SKV_ERR_ARG);
-  }
-  if (units == 0) return;
-  const int64_t active = active_waves(units, p.waves);
-  if ((int64_t)blockIdx.x >= active) return;
-  int64_t u = first_unit(blockIdx.x, units, active);
-  const int64_t end = first_unit(blockIdx.x + 1, units, active);
-
-  int64_t before = 0;  // units of the places before the one at hand
-  int chunk = 0;       // 64 places at a time
+  int64_t before = 0;  // units of the places before the 64 at hand
+  int chunk = 0;       // the first of them
   int32_t len_l = 0;
-  int64_t upto = 0;
-  auto look = [&](int c) {
-    len_l = place_len(g, a, p, c + lane, there, bad);
+  int64_t upto = 0;    // units up to and with the lane's place
+  bool there, bad;
+  auto look = [&]() {
+    len_l = place_len(g, a, p, chunk + lane, there, bad);
     upto = before + wave_scan(there ? (int64_t)tiles_of(len_l) * rows_of_place : 0);
   };
-  look(0);
+  for (;;) {
+    look();
+    if (bad && blockIdx.x == 0) set_status(status, SKV_ERR_ARG);
+    if (chunk + 64 >= p.n) break;
+    before = lane_of(upto, 63);
+    chunk += 64;
+  }
+  const int64_t units = lane_of(upto, 63);
+  const int64_t active = active_waves(units, p.waves);
+  if (units == 0 || (int64_t)blockIdx.x >= active) {
+    if (lane == 0) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  int64_t u = first_unit(blockIdx.x, units, active);
+  const int64_t end = first_unit(blockIdx.x + 1, units, active);
+  if (chunk > 0) {
+    before = 0;
+    chunk = 0;
+    look();
+  }
   const int64_t begun = u;
+  int4 split = make_int4(0, 0, 0, 0);
   while (u < end) {
     // the place of unit u: the first whose units reach beyond it
     uint64_t beyond = __builtin_amdgcn_ballot_w64(upto > u);
     while (beyond == 0) {
       before = lane_of(upto, 63);
       chunk += 64;
-      if (chunk >= p.n) return;  // only where lengths change under the call
-      look(chunk);
+      if (chunk >= p.n) {  // only where lengths change under the call
+        if (lane == 0) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+        return;
+      }
+      look();
       beyond = __builtin_amdgcn_ballot_w64(upto > u);
     }
     const int at = __builtin_ctzll(beyond);
@@ -327,9 +346,12 @@ __global__ __launch_bounds__(64) void k_attend(PGeo g, skv_pages a, int layer, A
     const int h = r / p.tiles_q, qt = r - h * p.tiles_q;
     const bool whole = ta == 0 && tb == tiles;
     const int slot = u == begun ? 0 : 1;
+    const int heads = min(kHeads, p.group - qt * kHeads);  // of this tile
+    if (ta == 0 && !whole)
+      split = split_of((int)(wave_with(u + tiles - 1, units, active) - blockIdx.x + 1), slot,
+                       (int32_t)((int64_t)i * p.q_heads + (int64_t)h * p.group + qt * kHeads), heads, h);
     u += tb - ta;
 
-    const int heads = min(kHeads, p.group - qt * kHeads);  // of this tile
     const int64_t qrow = (int64_t)i * p.q_heads + (int64_t)h * p.group + qt * kHeads + hd;
     float m = -INFINITY, l = 0.0f;
     f32x4 o[NV * CW];
@@ -448,7 +470,7 @@ __global__ __launch_bounds__(64) void k_attend(PGeo g, skv_pages a, int layer, A
           }
         if (p.lse && grp == 0) p.lse[qrow] = l == 0.0f ? -INFINITY : (m + __builtin_log2f(l)) * 0.693147180559945309417f;
       } else {
-        float *pp = p.part + ((int64_t)blockIdx.x * 2 + slot) * p.kept * (D + 2);
+        float *pp = p.part + ((int64_t)blockIdx.x * 2 + slot) * p.slot;
         float *po = pp + hd * D;
 #pragma unroll
         for (int c = 0; c < NV; ++c)
@@ -466,79 +488,89 @@ __global__ __launch_bounds__(64) void k_attend(PGeo g, skv_pages a, int layer, A
       }
     }
   }
+  if (lane == 0) p.split[blockIdx.x] = split;
 }
 
 // ---- the join ----
-// One workgroup per query head of a list place: nothing to do unless its row
-// spans waves.  out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w.
+// out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w over the waves w that a row
+// spans.  A workgroup takes 256 of the row's values, four to a lane; each of
+// its waves runs through every fourth partial sum with a running maximum as the main
+// kernel does, all loads of a round in flight at once, and the four are joined
+// in LDS.  Workgroups of waves that leave no such row end after one load.
 constexpr int kJoin = 256;
 
-__global__ __launch_bounds__(kJoin) void k_attend_join(PGeo g, skv_pages a, AttendArgs p) {
-  const int i = blockIdx.x / p.q_heads, j = blockIdx.x - i * p.q_heads;
+__global__ __launch_bounds__(kJoin) void k_attend_join(PGeo g, AttendArgs p) {
+  const int64_t w0 = blockIdx.x;
+  const int4 sp = p.split[w0];
+  const int parts = sp.x >> 1;
+  if (parts == 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int rows_of_place = g.heads * p.tiles_q;
-  bool there, bad;
-  int64_t units = 0, upto = 0;
-  int32_t len = 0;
-  for (int c = 0; c < p.n; c += 64) {
-    const int32_t ln = place_len(g, a, p, c + lane, there, bad);
-    const int64_t scan = units + wave_scan(there ? (int64_t)tiles_of(ln) * rows_of_place : 0);
-    if (i >= c && i < c + 64) {
-      if (!__builtin_amdgcn_readlane((int)there, i - c)) return;
-      len = __builtin_amdgcn_readlane(ln, i - c);
-      upto = lane_of(scan, i - c);
+  const int v = ((int)blockIdx.y * 64 + lane) * 4;  // the lane's first value of the row's heads * D
+  if ((int)blockIdx.y * 256 >= sp.z * g.D) return;
+  const bool in = v < sp.z * g.D;
+  const int hd = in ? v / g.D : 0;
+  // partial sum k: the first of wave w0 + k, but for the wave that the row begins inside of
+  auto part = [&](int k) { return p.part + ((w0 + k) * 2 + (k == 0 ? sp.x & 1 : 0)) * p.slot; };
+  float m = -INFINITY, l = 0.0f;
+  f32x4 o = {0, 0, 0, 0};
+  constexpr int R = 8;
+  for (int k0 = wave; k0 < parts; k0 += 4 * R) {
+    float ms[R], ls[R];
+    f32x4 os[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int k = k0 + 4 * r;
+      ms[r] = -INFINITY;
+      ls[r] = 0.0f;
+      os[r] = f32x4{0, 0, 0, 0};
+      if (k < parts && in) {
+        const float *pp = part(k);
+        ms[r] = pp[p.kept * g.D + hd];
+        ls[r] = pp[p.kept * (g.D + 1) + hd];
+        os[r] = *reinterpret_cast<const f32x4 *>(pp + v);
+      }
     }
-    units = lane_of(scan, 63);
+    float mn = m;
+#pragma unroll
+    for (int r = 0; r < R; ++r) mn = __builtin_fmaxf(mn, ms[r]);
+    const float mb = base_of(mn), f = __builtin_amdgcn_exp2f(m - mb);
+    m = mn;
+    l *= f;
+    o *= f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float e = __builtin_amdgcn_exp2f(ms[r] - mb);
+      l = __builtin_fmaf(e, ls[r], l);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[c] = __builtin_fmaf(e, os[r][c], o[c]);
+    }
   }
-  const int64_t active = active_waves(units, p.waves);
-  const int32_t tiles = tiles_of(len);
-  const int h = j / p.group, jg = j - h * p.group, qt = jg / kHeads, hd = jg - qt * kHeads;
-  const int64_t u0 = upto - (int64_t)tiles * rows_of_place + (int64_t)(h * p.tiles_q + qt) * tiles;
-  const int64_t w0 = wave_with(u0, units, active), w1 = wave_with(u0 + tiles - 1, units, active);
-  if (w0 == w1) return;
-  const int parts = (int)(w1 - w0 + 1);
-  const int slot0 = first_unit(w0, units, active) == u0 ? 0 : 1;
-  const int64_t stride = (int64_t)2 * p.kept * (g.D + 2);
-  // part k: wave w0 + k, in its first place but for the wave that the row begins inside of
-  const float *base = p.part + w0 * stride;
-  const int64_t shift = (int64_t)slot0 * p.kept * (g.D + 2);
-  auto part = [&](int k) { return base + k * stride + (k == 0 ? shift : 0); };
-
-  __shared__ float red[2][4];
-  __shared__ float acc[4][512];
-  float mx = -INFINITY;
-  for (int k = threadIdx.x; k < parts; k += kJoin) mx = __builtin_fmaxf(mx, part(k)[p.kept * g.D + hd]);
-  for (int d = 32; d; d >>= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, d));
-  if (lane == 0) red[0][wave] = mx;
+  __shared__ float sm[4][64], sl[4][64];
+  __shared__ f32x4 so[4][64];
+  sm[wave][lane] = m;
+  sl[wave][lane] = l;
+  so[wave][lane] = o;
   __syncthreads();
-  mx = __builtin_fmaxf(__builtin_fmaxf(red[0][0], red[0][1]), __builtin_fmaxf(red[0][2], red[0][3]));
+  if (wave > 0 || !in) return;
+  const float mx = __builtin_fmaxf(__builtin_fmaxf(sm[0][lane], sm[1][lane]), __builtin_fmaxf(sm[2][lane], sm[3][lane]));
   const float mb = base_of(mx);
-  float l = 0.0f;
-  for (int k = threadIdx.x; k < parts; k += kJoin)
-    l += __builtin_amdgcn_exp2f(part(k)[p.kept * g.D + hd] - mb) * part(k)[p.kept * (g.D + 1) + hd];
-  for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
-  if (lane == 0) red[1][wave] = l;
-  float o[8] = {};
-  for (int k = wave; k < parts; k += 4) {
-    const float f = __builtin_amdgcn_exp2f(part(k)[p.kept * g.D + hd] - mb);
-    const float *po = part(k) + hd * g.D;
+  l = 0.0f;
+  o = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      if (c * 64 + lane < g.D) o[c] = __builtin_fmaf(f, po[c * 64 + lane], o[c]);
+  for (int w = 0; w < 4; ++w) {
+    const float e = __builtin_amdgcn_exp2f(sm[w][lane] - mb);
+    l = __builtin_fmaf(e, sl[w][lane], l);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[c] = __builtin_fmaf(e, so[w][lane][c], o[c]);
   }
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    if (c * 64 + lane < g.D) acc[wave][c * 64 + lane] = o[c];
-  __syncthreads();
-  l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-  const float f = l == 0.0f ? 0.0f : (p.v_scale ? p.v_scale[h] : 1.0f) / l;
-  const int64_t qrow = (int64_t)i * p.q_heads + j;
-  for (int c = threadIdx.x; c < g.D; c += kJoin)
-    p.out[qrow * g.D + c] = (uint16_t)pack_bf16(((acc[0][c] + acc[1][c]) + (acc[2][c] + acc[3][c])) * f, 0.0f);
-  if (p.lse && threadIdx.x == 0) p.lse[qrow] = l == 0.0f ? -INFINITY : (mx + __builtin_log2f(l)) * 0.693147180559945309417f;
+  const float f = l == 0.0f ? 0.0f : (p.v_scale ? p.v_scale[sp.w] : 1.0f) / l;
+  const uint2 y = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
+  *reinterpret_cast<uint2 *>(p.out + (int64_t)sp.y * g.D + v) = y;
+  if (p.lse && v - hd * g.D == 0) p.lse[sp.y + hd] = l == 0.0f ? -INFINITY : (mx + __builtin_log2f(l)) * 0.693147180559945309417f;
 }
 
 int attend_waves() { return device_cu_count() * kWavesPerCu; }
+int slot_floats(const PGeo &g, int kept) { return kept * g.D + (2 * kept + 3) / 4 * 4; }
 
 }  // namespace
 
@@ -548,7 +580,7 @@ extern "C" int skv_attend_workspace_size(const skv_pages_shape *shape, int64_t q
   if (e != SKV_OK) return e;
   if (!bytes || q_heads < 1 || q_heads > (1 << 16) || q_heads % g.heads) return SKV_ERR_ARG;
   const int64_t group = q_heads / g.heads;
-  *bytes = sizeof(float) * (size_t)attend_waves() * 2 * (size_t)(group < kHeads ? group : kHeads) * (size_t)(g.D + 2);
+  *bytes = (size_t)attend_waves() * (2 * sizeof(float) * (size_t)slot_floats(g, (int)(group < kHeads ? group : kHeads)) + sizeof(int4));
   return SKV_OK;
 }
 
@@ -585,11 +617,13 @@ extern "C" int skv_attend(const skv_pages_shape *shape, const skv_pages *pages, 
   p.kept = p.group < kHeads ? p.group : kHeads;
   p.out = static_cast<uint16_t *>(out);
   p.lse = lse;
-  p.part = static_cast<float *>(workspace);
+  p.slot = slot_floats(g, p.kept);
   // no more waves than the longest sequences the table holds could use
   const __int128 most = ((__int128)n * g.heads * p.tiles_q * ((g.max_tokens + (int64_t)kTile - 1) / kTile) + kMinUnits - 1) / kMinUnits;
   const int all = attend_waves();
   p.waves = most < all ? (int)most : all;
+  p.split = static_cast<int4 *>(workspace);
+  p.part = reinterpret_cast<float *>(p.split + all);
   const dim3 grid((uint32_t)p.waves);
   hipStream_t st = static_cast<hipStream_t>(stream);
 #define SKV_ATTEND(F_, D_) case D_: k_attend<F_, D_><<<grid, 64, 0, st>>>(g, *pages, (int)layer, p, status); break
@@ -606,6 +640,6 @@ extern "C" int skv_attend(const skv_pages_shape *shape, const skv_pages *pages, 
 #undef SKV_ATTEND_ALL
 #undef SKV_ATTEND
   if (hipGetLastError() != hipSuccess) return SKV_ERR_HIP;
-  k_attend_join<<<dim3((uint32_t)(n * q_heads)), kJoin, 0, st>>>(g, *pages, p);
+  k_attend_join<<<dim3((uint32_t)p.waves, (uint32_t)((p.kept * g.D + 255) / 256)), kJoin, 0, st>>>(g, p);
   return hipGetLastError() == hipSuccess ? SKV_OK : SKV_ERR_HIP;
 }
