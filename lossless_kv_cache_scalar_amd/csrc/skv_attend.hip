@@ -1,13 +1,15 @@
 // skv_attend.hip -- attention of one new token per sequence over a paged cache.
 // Contract: skv.h.
 //
-// Work is cut into units: 32 tokens of one (sequence, KV head, tile of 16 query
-// heads).  The units of a call, in that order, are dealt out evenly to the
-// waves of the grid, a contiguous run to each, from the lengths on the device;
-// so the split over a sequence's length follows the lengths of the moment, and
-// one long sequence fills the chip as a batch of short ones does.  A row (sequence,
-// KV head, tile) that lies in one wave's run is finished there; one that
-// spans waves leaves partial sums, joined by a second launch.
+// Work is cut into units: 32 tokens of one row, a row being a sequence, a KV
+// head and a tile of its query heads.  The units of a call, row by row, are
+// dealt out evenly from the lengths on the device, a contiguous run to each
+// worker; so the split over a sequence's length follows the lengths of the moment,
+// and one long sequence fills the chip as a batch of short ones does.  A worker
+// is a workgroup of four waves, which share the tokens of each row and join
+// their sums in LDS, or, where rows are too short for four, a single wave.  A
+// row that lies in one worker's run is finished there; one that spans workers
+// leaves partial sums, joined by a second launch.
 //
 // A wave keeps all of its state in registers: for each query head the running
 // maximum m of the scores (times log2 e), the sum l of 2^(score - m), and the
@@ -25,13 +27,15 @@ namespace {
 
 constexpr int kTile = 32;    // tokens of a unit
 constexpr int kHeads = 16;   // query heads of a tile
-constexpr int kMinUnits = 2; // units that a wave gets at least
-constexpr int kWavesPerCu = 8;
+constexpr int kTeam = 4;     // waves of a workgroup
+constexpr int kTeamUnits = 4;  // units of an average row from which the waves of a workgroup share rows
+constexpr int kMinUnits = 1;   // units that a wave gets at least
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 struct AttendArgs {
@@ -42,20 +46,25 @@ struct AttendArgs {
   const int32_t *seqs;
   int n;
   int q_heads, group, tiles_q;  // query heads, per KV head, tiles of 16 of them
-  int kept;                     // heads of a partial sum: min(group, 16)
-  int waves;                    // of the main launch
+  int shared_q;                 // tiles of a row where waves share it: 1, 2 or 4, a wave to each
+  int kept;                     // heads of a shared row at most: min(group, 16 shared_q)
+  int blocks;                   // of the main launch
   uint16_t *out;
   float *lse;
-  int slot;                     // floats of a partial sum: O [kept][D], m [kept], l [kept], rounded up to 4
-  float *part;                  // [waves][2][slot]
-  int4 *split;                  // [waves] the row that begins in a wave's run and ends in another's (Split)
+  float *part;                  // [worker][2][slot_floats]: O [kept][D], m [kept], l [kept]
+  int4 *split;                  // [worker] the row that begins in its run and ends in another's
 };
 
-// what a wave leaves about such a row: waves it spans (0: there is none) and
-// where its first partial sum lies, its first query head's row in out, its
-// heads, its KV head
-__device__ __forceinline__ int4 split_of(int parts, int slot, int32_t qrow, int heads, int h) {
-  return make_int4(parts << 1 | slot, qrow, heads, h);
+// heads of a partial sum at most, where waves share rows or not; its floats
+__host__ __device__ __forceinline__ int kept_heads(int kept, bool team) { return team || kept < kHeads ? kept : kHeads; }
+__host__ __device__ __forceinline__ int slot_floats(int kept, int D) { return kept * D + (2 * kept + 3) / 4 * 4; }
+
+// A worker's number: its block's, or, where waves work alone, wave * blocks +
+// block.  What it leaves about a row that spans workers: how many (0: there is
+// none), where its own partial sum lies, whether workers are workgroups; the
+// row's first place in lse, its query heads, its KV head.
+__device__ __forceinline__ int4 split_of(int64_t parts, bool team, int slot, int32_t qrow, int heads, int h) {
+  return make_int4((int)parts << 2 | (team ? 2 : 0) | slot, qrow, heads, h);
 }
 
 // ---- the dealing out ----
@@ -99,14 +108,10 @@ __device__ __forceinline__ int64_t lane_of(int64_t v, int l) {
   return (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
 }
 
-// waves that take part: every one where there are units enough
-__device__ __forceinline__ int64_t active_waves(int64_t units, int waves) {
-  const int64_t n = units / kMinUnits;
-  return n < 1 ? 1 : (n < waves ? n : waves);
-}
+// runs: worker w of `active` has units [first_unit(w), first_unit(w + 1))
 __device__ __forceinline__ int64_t first_unit(int64_t w, int64_t units, int64_t active) { return w * units / active; }
-// the wave whose run holds unit u
-__device__ __forceinline__ int64_t wave_with(int64_t u, int64_t units, int64_t active) { return ((u + 1) * active - 1) / units; }
+// the worker whose run holds unit u
+__device__ __forceinline__ int64_t worker_with(int64_t u, int64_t units, int64_t active) { return ((u + 1) * active - 1) / units; }
 
 // ---- numbers ----
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -131,10 +136,16 @@ __device__ __forceinline__ float sum_over_rows(float v) {
   auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
+
 // m where it is a number to subtract: a row without any weight yet has m = -inf
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
 // ---- a unit's keys and values in registers ----
+// Each is read once, so past the caches: 7.0 TB/s against 6.1 for a plain read of 1 GiB.
+template <typename T>
+__device__ __forceinline__ T streamed(const uint8_t *p) { return __builtin_nontemporal_load(reinterpret_cast<const T *>(p)); }
+
 // K, operand A of a 16x16x32 product: lane l holds token l % 16, eight of 32
 // channels by l / 16.  bf16: channels in order; e4m3: a 16-byte load holds the
 // lane's channels of two products (which channels form a product does not
@@ -159,9 +170,9 @@ struct Keys {
       for (int j = 0; j < NL; ++j) {
         if (row >= 4 * bytes || in) {
           if (wide) {
-            r[s][j] = *reinterpret_cast<const u32x4 *>(b + off + j * 64);
+            r[s][j] = streamed<u32x4>(b + off + j * 64);
           } else {
-            const uint2 v = *reinterpret_cast<const uint2 *>(b + off);
+            const u32x2 v = streamed<u32x2>(b + off);
             r[s][j] = u32x4{v.x, v.y, 0, 0};
           }
         } else {
@@ -206,11 +217,11 @@ struct Values {
       const uint8_t *b = (i < 4 ? b0 : b1) + off + (i & 3) * row;
       if (D >= 16 || c < D) {
         if (bytes == 16) {
-          const u32x4 v = *reinterpret_cast<const u32x4 *>(b);
+          const u32x4 v = streamed<u32x4>(b);
 #pragma unroll
           for (int k = 0; k < W; ++k) w[i][k] = v[k];
         } else if (bytes == 8) {
-          const uint2 v = *reinterpret_cast<const uint2 *>(b);
+          const u32x2 v = streamed<u32x2>(b);
           w[i][0] = v.x;
           w[i][W - 1] = v.y;
         } else if (bytes == 4) {
@@ -280,88 +291,106 @@ struct Ids {
   }
 };
 
+// workgroups of a CU: their registers (to 128 channels at most 256 each) allow two, or one
+constexpr int blocks_per_cu(int D) { return D <= 128 ? 2 : 1; }
+
 template <int FMT, int D>
-__global__ __launch_bounds__(64) void k_attend(PGeo g, skv_pages a, int layer, AttendArgs p, int32_t *status) {
+__global__ __launch_bounds__(64 * kTeam, blocks_per_cu(D)) void k_attend(PGeo g, skv_pages a, int layer, AttendArgs p,
+                                                                        int32_t *status) {
   using K = Keys<FMT, D>;
   using V = Values<FMT, D>;
   constexpr int KB = K::KB, CW = V::CW;
   constexpr int NV = D < 128 ? 1 : D / 128;  // chunks of 128 channels
   constexpr int row = K::row;
-  const int lane = threadIdx.x, hd = lane & 15, grp = lane >> 4;
-  const int rows_of_place = g.heads * p.tiles_q;
+  constexpr int LD = D + 4;                  // sixteen heads' rows then lie in different banks
+  __shared__ float os[kTeam][kHeads][LD];
+  __shared__ float sm[kTeam][kHeads], sl[kTeam][kHeads];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = lane & 15, grp = lane >> 4;
 
-  // units in all, and the place that this wave's run begins in
-  int64_t before = 0;  // units of the places before the 64 at hand
+  // units in all, and the place that this worker's run begins in
+  int64_t before = 0;  // tiles of 32 tokens in the places before the 64 at hand
+  int64_t places = 0;
   int chunk = 0;       // the first of them
   int32_t len_l = 0;
-  int64_t upto = 0;    // units up to and with the lane's place
+  int64_t upto = 0;    // tiles up to and with the lane's place
   bool there, bad;
   auto look = [&]() {
     len_l = place_len(g, a, p, chunk + lane, there, bad);
-    upto = before + wave_scan(there ? (int64_t)tiles_of(len_l) * rows_of_place : 0);
+    upto = before + wave_scan(there ? (int64_t)tiles_of(len_l) : 0);
   };
   for (;;) {
     look();
+    places += __builtin_popcountll(__builtin_amdgcn_ballot_w64(there));
     if (bad && blockIdx.x == 0) set_status(status, SKV_ERR_ARG);
     if (chunk + 64 >= p.n) break;
     before = lane_of(upto, 63);
     chunk += 64;
   }
-  const int64_t units = lane_of(upto, 63);
-  const int64_t active = active_waves(units, p.waves);
-  if (units == 0 || (int64_t)blockIdx.x >= active) {
-    if (lane == 0) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+  const int64_t all = lane_of(upto, 63);
+  const bool team = all >= kTeamUnits * places;
+  const int row_tiles = team ? p.shared_q : 1;                               // tiles of query heads in a row
+  const int rows_of_head = (p.tiles_q + row_tiles - 1) / row_tiles, rows_of_place = g.heads * rows_of_head;
+  const int64_t units = all * rows_of_place;
+  const int64_t most = team ? p.blocks : (int64_t)p.blocks * kTeam;
+  const int64_t fit = units / (team ? kMinUnits * kTeam : kMinUnits);
+  const int64_t active = fit < 1 ? 1 : (fit < most ? fit : most);
+  const int64_t me = team ? blockIdx.x : (int64_t)wave * p.blocks + blockIdx.x;
+  int4 *const note = &p.split[(int64_t)wave * p.blocks + blockIdx.x];
+  int4 split = make_int4(0, 0, 0, 0);
+  if (units == 0 || me >= active) {
+    if (lane == 0) *note = split;
     return;
   }
-  int64_t u = first_unit(blockIdx.x, units, active);
-  const int64_t end = first_unit(blockIdx.x + 1, units, active);
+  int64_t u = first_unit(me, units, active);
+  const int64_t end = first_unit(me + 1, units, active);
   if (chunk > 0) {
     before = 0;
     chunk = 0;
     look();
   }
   const int64_t begun = u;
-  int4 split = make_int4(0, 0, 0, 0);
   while (u < end) {
     // the place of unit u: the first whose units reach beyond it
-    uint64_t beyond = __builtin_amdgcn_ballot_w64(upto > u);
-    while (beyond == 0) {
+    uint64_t beyond = __builtin_amdgcn_ballot_w64(upto * rows_of_place > u);
+    while (beyond == 0 && chunk + 64 < p.n) {
       before = lane_of(upto, 63);
       chunk += 64;
-      if (chunk >= p.n) {  // only where lengths change under the call
-        if (lane == 0) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
-        return;
-      }
       look();
-      beyond = __builtin_amdgcn_ballot_w64(upto > u);
+      beyond = __builtin_amdgcn_ballot_w64(upto * rows_of_place > u);
     }
+    if (beyond == 0) break;  // only where lengths change under the call
     const int at = __builtin_ctzll(beyond);
     const int i = chunk + at;
     const int32_t len = __builtin_amdgcn_readlane(len_l, at);
     const int32_t tiles = tiles_of(len);
-    const int64_t in_place = u - (lane_of(upto, at) - (int64_t)tiles * rows_of_place);
-    const int r = (int)(in_place / tiles);             // (KV head, tile of query heads)
+    const int64_t in_place = u - (lane_of(upto, at) - tiles) * rows_of_place;
+    const int r = (int)(in_place / tiles);             // (KV head, its row)
     const int32_t ta = (int32_t)(in_place - (int64_t)r * tiles);
     const int32_t tb = (int32_t)min((int64_t)tiles, ta + (end - u));
-    const int h = r / p.tiles_q, qt = r - h * p.tiles_q;
+    const int h = r / rows_of_head, q0 = (r - h * rows_of_head) * row_tiles * kHeads;  // first query head of the row
     const bool whole = ta == 0 && tb == tiles;
     const int slot = u == begun ? 0 : 1;
-    const int heads = min(kHeads, p.group - qt * kHeads);  // of this tile
+    const int row_heads = min(row_tiles * kHeads, p.group - q0);
+    const int64_t row_at = (int64_t)i * p.q_heads + (int64_t)h * p.group + q0;
     if (ta == 0 && !whole)
-      split = split_of((int)(wave_with(u + tiles - 1, units, active) - blockIdx.x + 1), slot,
-                       (int32_t)((int64_t)i * p.q_heads + (int64_t)h * p.group + qt * kHeads), heads, h);
+      split = split_of(worker_with(u + tiles - 1, units, active) - me + 1, team, slot, (int32_t)row_at, row_heads, h);
     u += tb - ta;
 
-    const int64_t qrow = (int64_t)i * p.q_heads + (int64_t)h * p.group + qt * kHeads + hd;
+    // this wave's tile of query heads, and its part of the tokens
+    const int my_tile = team ? wave & (p.shared_q - 1) : 0;
+    const int parts = team ? kTeam / p.shared_q : 1, part = team ? wave / p.shared_q : 0;
+    const int32_t wa = ta + (int32_t)((int64_t)(tb - ta) * part / parts);
+    const int32_t wb = ta + (int32_t)((int64_t)(tb - ta) * (part + 1) / parts);
+    const int heads = min(kHeads, row_heads - my_tile * kHeads);  // none where it has no tile
     float m = -INFINITY, l = 0.0f;
     f32x4 o[NV * CW];
 #pragma unroll
     for (int k = 0; k < NV * CW; ++k) o[k] = f32x4{0, 0, 0, 0};
 
-    if (len > 0) {
+    if (len > 0 && heads > 0 && wa < wb) {
       const int32_t s = p.seqs[i];
       bf16x8 qf[KB];
-      const uint16_t *qp = p.q + (int64_t)i * p.q_stride + (int64_t)(h * p.group + qt * kHeads + hd) * D;
+      const uint16_t *qp = p.q + (int64_t)i * p.q_stride + (int64_t)(h * p.group + q0 + my_tile * kHeads + hd) * D;
 #pragma unroll
       for (int j = 0; j < KB; ++j) {
         u32x4 v = {0, 0, 0, 0};
@@ -369,12 +398,12 @@ __global__ __launch_bounds__(64) void k_attend(PGeo g, skv_pages a, int layer, A
         if (hd < heads && c < D) v = *reinterpret_cast<const u32x4 *>(qp + c);
         qf[j] = __builtin_bit_cast(bf16x8, v);
       }
-      const float sc = p.scale * (p.k_scale ? p.k_scale[h] : 1.0f) * 1.44269504088896340736f;
+      const float sc = p.scale * (p.k_scale ? p.k_scale[h] : 1.0f) * kLog2e;
 
       Ids ids;
       ids.row = a.table + (int64_t)s * g.max_pages;
-      ids.first = ta * kTile >> g.log2P;
-      ids.last = (int32_t)((min((uint32_t)tb * kTile, (uint32_t)len) - 1) >> g.log2P);
+      ids.first = wa * kTile >> g.log2P;
+      ids.last = (int32_t)((min((uint32_t)wb * kTile, (uint32_t)len) - 1) >> g.log2P);
       ids.n_pages = g.n_pages;
       ids.fetch(status);
       const uint8_t *kbase = static_cast<const uint8_t *>(a.pool) + (int64_t)layer * g.n_pages * g.page_bytes + (int64_t)h * g.P * row;
@@ -387,9 +416,9 @@ __global__ __launch_bounds__(64) void k_attend(PGeo g, skv_pages a, int layer, A
       };
 
       K keys;
-      const uint8_t *b0 = half(ta, 0), *b1 = half(ta, 1);
+      const uint8_t *b0 = half(wa, 0), *b1 = half(wa, 1);
       keys.load(b0, b1);
-      for (int32_t t = ta; t < tb; ++t) {
+      for (int32_t t = wa; t < wb; ++t) {
         const int left = len - t * kTile;  // tokens from here on
         V vals;
         vals.load(b0 + to_v, b1 + to_v, 0);
@@ -399,7 +428,7 @@ __global__ __launch_bounds__(64) void k_attend(PGeo g, skv_pages a, int layer, A
         for (int j = 0; j < KB; ++j)
 #pragma unroll
           for (int b = 0; b < 2; ++b) z[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(keys.operand(b, j), qf[j], z[b], 0, 0, 0);
-        if (t + 1 < tb) {
+        if (t + 1 < wb) {
           b0 = half(t + 1, 0);
           b1 = half(t + 1, 1);
           keys.load(b0, b1);
@@ -450,83 +479,103 @@ __global__ __launch_bounds__(64) void k_attend(PGeo g, skv_pages a, int layer, A
       l = sum_over_rows(l);
     }
 
-    // a lane has channels 128 c + CW (4 grp + x) + k of its head in o[c CW + k][x]
+    // To LDS: a lane has channels 128 c + CW (4 grp + x) + k of its head in
+    // o[c CW + k][x].  Where waves share the row, those of a tile are joined there.
     if (hd < heads) {
-      if (whole) {
-        const float f = l == 0.0f ? 0.0f : (p.v_scale ? p.v_scale[h] : 1.0f) / l;
-        uint16_t *op = p.out + qrow * D;
 #pragma unroll
-        for (int c = 0; c < NV; ++c)
+      for (int c = 0; c < NV; ++c)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int ch = 128 * c + CW * (4 * grp + x);
-            if (CW == 1) {
-              if (ch < D) op[ch] = (uint16_t)pack_bf16(o[0][x] * f, 0.0f);
-            } else {
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
-              for (int k = 0; k < CW; k += 2)
-                *reinterpret_cast<uint32_t *>(op + ch + k) = pack_bf16(o[c * CW + k][x] * f, o[c * CW + (CW > 1 ? k + 1 : 0)][x] * f);
-            }
+          for (int k = 0; k < CW; ++k) {
+            const int ch = 128 * c + CW * (4 * grp + x) + k;
+            if (D >= 16 || ch < D) os[wave][hd][ch] = o[c * CW + k][x];
           }
-        if (p.lse && grp == 0) p.lse[qrow] = l == 0.0f ? -INFINITY : (m + __builtin_log2f(l)) * 0.693147180559945309417f;
+      if (grp == 0) {
+        sm[wave][hd] = m;
+        sl[wave][hd] = l;
+      }
+    }
+    if (team) __syncthreads();
+    else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int kept = kept_heads(p.kept, team);
+    float *pp = p.part + (me * 2 + slot) * slot_floats(kept, D);
+    const float vs = p.v_scale ? p.v_scale[h] : 1.0f;
+    for (int v = (team ? (int)threadIdx.x : lane) * 4; v < row_heads * D; v += (team ? kTeam * 64 : 64) * 4) {
+      const int hh = v / D, ch = v - hh * D;
+      const int w0 = team ? hh / kHeads : wave, hw = hh & (kHeads - 1);
+      float mx = sm[w0][hw];
+      for (int k = 1; k < parts; ++k) mx = __builtin_fmaxf(mx, sm[w0 + k * p.shared_q][hw]);
+      const float mb = base_of(mx);
+      float ls = 0.0f;
+      f32x4 ov = {0, 0, 0, 0};
+      for (int k = 0; k < parts; ++k) {
+        const int w = w0 + k * p.shared_q;
+        const float e = __builtin_amdgcn_exp2f(sm[w][hw] - mb);
+        ls = __builtin_fmaf(e, sl[w][hw], ls);
+        const f32x4 x = *reinterpret_cast<const f32x4 *>(&os[w][hw][ch]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ov[c] = __builtin_fmaf(e, x[c], ov[c]);
+      }
+      if (whole) {
+        const float f = ls == 0.0f ? 0.0f : vs / ls;
+        *reinterpret_cast<uint2 *>(p.out + (row_at + hh) * D + ch) = make_uint2(pack_bf16(ov[0] * f, ov[1] * f), pack_bf16(ov[2] * f, ov[3] * f));
+        if (p.lse && ch == 0) p.lse[row_at + hh] = ls == 0.0f ? -INFINITY : (mx + __builtin_log2f(ls)) * kLn2;
       } else {
-        float *pp = p.part + ((int64_t)blockIdx.x * 2 + slot) * p.slot;
-        float *po = pp + hd * D;
-#pragma unroll
-        for (int c = 0; c < NV; ++c)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int k = 0; k < CW; ++k) {
-              const int ch = 128 * c + CW * (4 * grp + x) + k;
-              if (ch < D) po[ch] = o[c * CW + k][x];
-            }
-        if (grp == 0) {
-          pp[p.kept * D + hd] = m;
-          pp[p.kept * (D + 1) + hd] = l;
+        *reinterpret_cast<f32x4 *>(pp + v) = ov;
+        if (ch == 0) {
+          pp[kept * D + hh] = mx;
+          pp[kept * (D + 1) + hh] = ls;
         }
       }
     }
+    if (team) __syncthreads();
+    else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
-  if (lane == 0) p.split[blockIdx.x] = split;
+  // of a workgroup the first wave's word says it all
+  if (lane == 0) *note = team && wave > 0 ? make_int4(0, 0, 0, 0) : split;
 }
 
 // ---- the join ----
-// out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w over the waves w that a row
-// spans.  A workgroup takes 256 of the row's values, four to a lane; each of
-// its waves runs through every fourth partial sum with a running maximum as the main
+// out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w over the workers w that a
+// row spans.  A workgroup takes 256 of the row's values, four to a lane; each of its
+// waves runs through every fourth partial sum with a running maximum as the main
 // kernel does, all loads of a round in flight at once, and the four are joined
-// in LDS.  Workgroups of waves that leave no such row end after one load.
+// in LDS.  Rows of single waves have few partial sums, and a wave each.
+// Workgroups of workers that leave no such row end after one load.
 constexpr int kJoin = 256;
 
 __global__ __launch_bounds__(kJoin) void k_attend_join(PGeo g, AttendArgs p) {
-  const int64_t w0 = blockIdx.x;
-  const int4 sp = p.split[w0];
-  const int parts = sp.x >> 1;
-  if (parts == 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int4 first = p.split[blockIdx.x], own = p.split[(int64_t)wave * p.blocks + blockIdx.x];
+  const bool team = first.x & 2;
+  const int4 sp = team ? first : own;
+  const int parts = sp.x >> 2;
+  if (parts == 0 || (int)blockIdx.y * 256 >= sp.z * g.D) return;
+  const int64_t w0 = team ? blockIdx.x : (int64_t)wave * p.blocks + blockIdx.x;
+  const int k_first = team ? wave : 0, k_step = team ? 4 : 1;
   const int v = ((int)blockIdx.y * 64 + lane) * 4;  // the lane's first value of the row's heads * D
-  if ((int)blockIdx.y * 256 >= sp.z * g.D) return;
   const bool in = v < sp.z * g.D;
   const int hd = in ? v / g.D : 0;
-  // partial sum k: the first of wave w0 + k, but for the wave that the row begins inside of
-  auto part = [&](int k) { return p.part + ((w0 + k) * 2 + (k == 0 ? sp.x & 1 : 0)) * p.slot; };
+  // partial sum k: the first of worker w0 + k, but for the one that the row begins inside of
+  const int kept = kept_heads(p.kept, team), floats = slot_floats(kept, g.D);
+  auto part = [&](int k) { return p.part + ((w0 + k) * 2 + (k == 0 ? sp.x & 1 : 0)) * floats; };
   float m = -INFINITY, l = 0.0f;
   f32x4 o = {0, 0, 0, 0};
   constexpr int R = 8;
-  for (int k0 = wave; k0 < parts; k0 += 4 * R) {
+  for (int k0 = k_first; k0 < parts; k0 += k_step * R) {
     float ms[R], ls[R];
     f32x4 os[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int k = k0 + 4 * r;
+      const int k = k0 + k_step * r;
       ms[r] = -INFINITY;
       ls[r] = 0.0f;
       os[r] = f32x4{0, 0, 0, 0};
       if (k < parts && in) {
         const float *pp = part(k);
-        ms[r] = pp[p.kept * g.D + hd];
-        ls[r] = pp[p.kept * (g.D + 1) + hd];
+        ms[r] = pp[kept * g.D + hd];
+        ls[r] = pp[kept * (g.D + 1) + hd];
         os[r] = *reinterpret_cast<const f32x4 *>(pp + v);
       }
     }
@@ -547,30 +596,48 @@ __global__ __launch_bounds__(kJoin) void k_attend_join(PGeo g, AttendArgs p) {
   }
   __shared__ float sm[4][64], sl[4][64];
   __shared__ f32x4 so[4][64];
-  sm[wave][lane] = m;
-  sl[wave][lane] = l;
-  so[wave][lane] = o;
-  __syncthreads();
-  if (wave > 0 || !in) return;
-  const float mx = __builtin_fmaxf(__builtin_fmaxf(sm[0][lane], sm[1][lane]), __builtin_fmaxf(sm[2][lane], sm[3][lane]));
-  const float mb = base_of(mx);
-  l = 0.0f;
-  o = f32x4{0, 0, 0, 0};
+  if (team) {
+    sm[wave][lane] = m;
+    sl[wave][lane] = l;
+    so[wave][lane] = o;
+    __syncthreads();
+    if (wave > 0) return;
+    const float mx = __builtin_fmaxf(__builtin_fmaxf(sm[0][lane], sm[1][lane]), __builtin_fmaxf(sm[2][lane], sm[3][lane]));
+    const float mb = base_of(mx);
+    l = 0.0f;
+    o = f32x4{0, 0, 0, 0};
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float e = __builtin_amdgcn_exp2f(sm[w][lane] - mb);
-    l = __builtin_fmaf(e, sl[w][lane], l);
+    for (int w = 0; w < 4; ++w) {
+      const float e = __builtin_amdgcn_exp2f(sm[w][lane] - mb);
+      l = __builtin_fmaf(e, sl[w][lane], l);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] = __builtin_fmaf(e, so[w][lane][c], o[c]);
+      for (int c = 0; c < 4; ++c) o[c] = __builtin_fmaf(e, so[w][lane][c], o[c]);
+    }
+    m = mx;
   }
+  if (!in) return;
   const float f = l == 0.0f ? 0.0f : (p.v_scale ? p.v_scale[sp.w] : 1.0f) / l;
   const uint2 y = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
   *reinterpret_cast<uint2 *>(p.out + (int64_t)sp.y * g.D + v) = y;
-  if (p.lse && v - hd * g.D == 0) p.lse[sp.y + hd] = l == 0.0f ? -INFINITY : (mx + __builtin_log2f(l)) * 0.693147180559945309417f;
+  if (p.lse && v - hd * g.D == 0) p.lse[sp.y + hd] = l == 0.0f ? -INFINITY : (m + __builtin_log2f(l)) * kLn2;
 }
 
-int attend_waves() { return device_cu_count() * kWavesPerCu; }
-int slot_floats(const PGeo &g, int kept) { return kept * g.D + (2 * kept + 3) / 4 * 4; }
+struct Plan {
+  int group, tiles_q, shared_q, kept, blocks;
+  int64_t bytes;
+};
+
+Plan attend_plan(const PGeo &g, int64_t q_heads) {
+  Plan p;
+  p.group = (int)(q_heads / g.heads);
+  p.tiles_q = (p.group + kHeads - 1) / kHeads;
+  p.shared_q = p.tiles_q == 1 ? 1 : (p.tiles_q == 2 ? 2 : kTeam);
+  p.kept = p.group < kHeads * p.shared_q ? p.group : kHeads * p.shared_q;
+  p.blocks = device_cu_count() * blocks_per_cu(g.D);
+  const int64_t shared = slot_floats(p.kept, g.D), alone = (int64_t)kTeam * slot_floats(kept_heads(p.kept, false), g.D);
+  p.bytes = p.blocks * (kTeam * (int64_t)sizeof(int4) + 2 * (int64_t)sizeof(float) * (shared > alone ? shared : alone));
+  return p;
+}
 
 }  // namespace
 
@@ -579,8 +646,7 @@ extern "C" int skv_attend_workspace_size(const skv_pages_shape *shape, int64_t q
   int e = make_pgeo(shape, g);
   if (e != SKV_OK) return e;
   if (!bytes || q_heads < 1 || q_heads > (1 << 16) || q_heads % g.heads) return SKV_ERR_ARG;
-  const int64_t group = q_heads / g.heads;
-  *bytes = (size_t)attend_waves() * (2 * sizeof(float) * (size_t)slot_floats(g, (int)(group < kHeads ? group : kHeads)) + sizeof(int4));
+  *bytes = (size_t)attend_plan(g, q_heads).bytes;
   return SKV_OK;
 }
 
@@ -612,21 +678,21 @@ extern "C" int skv_attend(const skv_pages_shape *shape, const skv_pages *pages, 
   p.seqs = seqs;
   p.n = (int)n;
   p.q_heads = (int)q_heads;
-  p.group = (int)(q_heads / g.heads);
-  p.tiles_q = (p.group + kHeads - 1) / kHeads;
-  p.kept = p.group < kHeads ? p.group : kHeads;
+  const Plan plan = attend_plan(g, q_heads);
+  p.group = plan.group;
+  p.tiles_q = plan.tiles_q;
+  p.shared_q = plan.shared_q;
+  p.kept = plan.kept;
   p.out = static_cast<uint16_t *>(out);
   p.lse = lse;
-  p.slot = slot_floats(g, p.kept);
-  // no more waves than the longest sequences the table holds could use
-  const __int128 most = ((__int128)n * g.heads * p.tiles_q * ((g.max_tokens + (int64_t)kTile - 1) / kTile) + kMinUnits - 1) / kMinUnits;
-  const int all = attend_waves();
-  p.waves = most < all ? (int)most : all;
+  // no more workgroups than the longest sequences that the table holds could use
+  const __int128 units = (__int128)n * g.heads * plan.tiles_q * (((int64_t)g.max_tokens + kTile - 1) / kTile);
+  p.blocks = units < plan.blocks ? (int)units : plan.blocks;
   p.split = static_cast<int4 *>(workspace);
-  p.part = reinterpret_cast<float *>(p.split + all);
-  const dim3 grid((uint32_t)p.waves);
+  p.part = reinterpret_cast<float *>(p.split + (int64_t)p.blocks * kTeam);
+  const dim3 grid((uint32_t)p.blocks);
   hipStream_t st = static_cast<hipStream_t>(stream);
-#define SKV_ATTEND(F_, D_) case D_: k_attend<F_, D_><<<grid, 64, 0, st>>>(g, *pages, (int)layer, p, status); break
+#define SKV_ATTEND(F_, D_) case D_: k_attend<F_, D_><<<grid, 64 * kTeam, 0, st>>>(g, *pages, (int)layer, p, status); break
 #define SKV_ATTEND_ALL(F_) \
   switch (g.D) { \
     SKV_ATTEND(F_, 8); SKV_ATTEND(F_, 16); SKV_ATTEND(F_, 32); SKV_ATTEND(F_, 64); \
@@ -640,6 +706,6 @@ extern "C" int skv_attend(const skv_pages_shape *shape, const skv_pages *pages, 
 #undef SKV_ATTEND_ALL
 #undef SKV_ATTEND
   if (hipGetLastError() != hipSuccess) return SKV_ERR_HIP;
-  k_attend_join<<<dim3((uint32_t)p.waves, (uint32_t)((p.kept * g.D + 255) / 256)), kJoin, 0, st>>>(g, p);
+  k_attend_join<<<dim3((uint32_t)p.blocks, (uint32_t)((p.kept * g.D + 255) / 256)), kJoin, 0, st>>>(g, p);
   return hipGetLastError() == hipSuccess ? SKV_OK : SKV_ERR_HIP;
 }

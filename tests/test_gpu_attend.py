@@ -140,6 +140,17 @@ def test_many_rows(rows):
     c.compare(0, q, seqs, out, lse)
 
 
+@pytest.mark.parametrize("fmt,D,kv_heads,group", [(0, 128, 8, 2), (1, 64, 4, 20), (0, 512, 2, 33)])
+def test_one_long_row_among_many_short_ones(fmt, D, kv_heads, group):
+    """Rows too short to be shared by waves, and one that spans many of them."""
+    lens = [(11 * i) % 61 for i in range(150)] + [9001]
+    c = Case(fmt, lens, D, 16, kv_heads, kv_heads * group, layers=1)
+    seqs = list(range(0, 150, 2)) + [150, -1] + list(range(1, 150, 2)) + list(range(40))
+    q = c.q(len(seqs))
+    out, lse = c.attend(0, q, seqs)
+    c.compare(0, q, seqs, out, lse)
+
+
 def test_all_rows_padded_or_empty():
     c = Case(0, [0, 5], 64, 16, 2, 4)
     for seqs in ([-1], [0], [-1, -1, 0], [2, 0]):
