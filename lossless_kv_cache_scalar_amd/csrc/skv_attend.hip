@@ -4,12 +4,12 @@
 // Work is cut into units: 32 tokens of one row, a row being a sequence, a KV
 // head and a tile of its query heads.  The units of a call, row by row, are
 // dealt out evenly from the lengths on the device, a contiguous run to each
-// worker; so the split over a sequence's length follows the lengths of the moment,
-// and one long sequence fills the chip as a batch of short ones does.  A worker
-// is a workgroup of four waves, which share the tokens of each row and join
-// their sums in LDS, or, where rows are too short for four, a single wave.  A
-// row that lies in one worker's run is finished there; one that spans workers
-// leaves partial sums, joined by a second launch.
+// workgroup; so the split over a sequence's length follows the lengths of the moment,
+// and one long sequence fills the chip as a batch of short ones does.  Within a
+// workgroup the run is dealt out to the waves in the same way: a wave works
+// through its part alone, and a row that spans waves is joined in LDS at the end.
+// A row that lies in one workgroup's run is finished there; one that spans
+// workgroups leaves partial sums, joined by a second launch.
 //
 // A wave keeps all of its state in registers: for each query head the running
 // maximum m of the scores (times log2 e), the sum l of 2^(score - m), and the
@@ -27,9 +27,11 @@ namespace {
 
 constexpr int kTile = 32;    // tokens of a unit
 constexpr int kHeads = 16;   // query heads of a tile
-constexpr int kTeam = 4;     // waves of a workgroup
-constexpr int kTeamUnits = 4;  // units of an average row from which the waves of a workgroup share rows
-constexpr int kMinUnits = 1;   // units that a wave gets at least
+constexpr int kMinUnits = 4; // units of a workgroup at least
+// waves of a workgroup (LDS holds two partial sums of each) and workgroups of a
+// CU (registers: to 128 channels at most 256 each)
+__host__ __device__ constexpr int waves_of(int D) { return D <= 256 ? 4 : 2; }
+__host__ __device__ constexpr int blocks_per_cu(int D) { return D <= 128 ? 2 : 1; }
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -46,26 +48,25 @@ struct AttendArgs {
   const int32_t *seqs;
   int n;
   int q_heads, group, tiles_q;  // query heads, per KV head, tiles of 16 of them
-  int shared_q;                 // tiles of a row where waves share it: 1, 2 or 4, a wave to each
-  int kept;                     // heads of a shared row at most: min(group, 16 shared_q)
+  int shared_q;                 // tiles of a row, a wave to each: 1, 2 or 4
+  int kept;                     // heads of a row at most: min(group, 16 shared_q)
   int blocks;                   // of the main launch
   uint16_t *out;
   float *lse;
-  float *part;                  // [worker][2][slot_floats]: O [kept][D], m [kept], l [kept]
-  int4 *split;                  // [worker] the row that begins in its run and ends in another's
+  int slot;                     // floats of a partial sum: O [kept][D], m [kept], l [kept], rounded up to 4
+  float *part;                  // [block][2][slot]
+  int4 *split;                  // [block] the row that begins in its run and ends in another's: workgroups that it
+                                // spans (0: there is none) * 2 + place of the first partial sum, its first place in
+                                // lse, its query heads, its KV head
 };
 
-// heads of a partial sum at most, where waves share rows or not; its floats
-__host__ __device__ __forceinline__ int kept_heads(int kept, bool team) { return team || kept < kHeads ? kept : kHeads; }
-__host__ __device__ __forceinline__ int slot_floats(int kept, int D) { return kept * D + (2 * kept + 3) / 4 * 4; }
-
-// A worker's number: its block's, or, where waves work alone, wave * blocks +
-// block.  What it leaves about a row that spans workers: how many (0: there is
-// none), where its own partial sum lies, whether workers are workgroups; the
-// row's first place in lse, its query heads, its KV head.
-__device__ __forceinline__ int4 split_of(int64_t parts, bool team, int slot, int32_t qrow, int heads, int h) {
-  return make_int4((int)parts << 2 | (team ? 2 : 0) | slot, qrow, heads, h);
-}
+// a row of which a wave has a part
+struct Row {
+  int64_t u0;      // its first unit
+  int32_t tiles;   // its units; 0: no row
+  int32_t at;      // its first place in lse
+  int32_t heads, h;
+};
 
 // ---- the dealing out ----
 // units of list place i; 0 for padding.  An empty sequence has one unit, whose
@@ -108,10 +109,10 @@ __device__ __forceinline__ int64_t lane_of(int64_t v, int l) {
   return (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
 }
 
-// runs: worker w of `active` has units [first_unit(w), first_unit(w + 1))
+// runs: workgroup w of `active` has units [first_unit(w), first_unit(w + 1))
 __device__ __forceinline__ int64_t first_unit(int64_t w, int64_t units, int64_t active) { return w * units / active; }
-// the worker whose run holds unit u
-__device__ __forceinline__ int64_t worker_with(int64_t u, int64_t units, int64_t active) { return ((u + 1) * active - 1) / units; }
+// the workgroup whose run holds unit u
+__device__ __forceinline__ int64_t block_with(int64_t u, int64_t units, int64_t active) { return ((u + 1) * active - 1) / units; }
 
 // ---- numbers ----
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -291,103 +292,90 @@ struct Ids {
   }
 };
 
-// workgroups of a CU: their registers (to 128 channels at most 256 each) allow two, or one
-constexpr int blocks_per_cu(int D) { return D <= 128 ? 2 : 1; }
-
 template <int FMT, int D>
-__global__ __launch_bounds__(64 * kTeam, blocks_per_cu(D)) void k_attend(PGeo g, skv_pages a, int layer, AttendArgs p,
-                                                                        int32_t *status) {
+__global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(PGeo g, skv_pages a, int layer, AttendArgs p,
+                                                                              int32_t *status) {
   using K = Keys<FMT, D>;
   using V = Values<FMT, D>;
   constexpr int KB = K::KB, CW = V::CW;
   constexpr int NV = D < 128 ? 1 : D / 128;  // chunks of 128 channels
   constexpr int row = K::row;
+  constexpr int NW = waves_of(D);
   constexpr int LD = D + 4;                  // sixteen heads' rows then lie in different banks
-  __shared__ float os[kTeam][kHeads][LD];
-  __shared__ float sm[kTeam][kHeads], sl[kTeam][kHeads];
+  __shared__ float os[NW][2][kHeads][LD];
+  __shared__ float sm[NW][2][kHeads], sl[NW][2][kHeads];
+  __shared__ Row rows[NW][2];                // by part of the run
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = lane & 15, grp = lane >> 4;
 
-  // units in all, and the place that this worker's run begins in
-  int64_t before = 0;  // tiles of 32 tokens in the places before the 64 at hand
-  int64_t places = 0;
+  // units in all, and the place that this workgroup's run begins in
+  const int rows_of_head = (p.tiles_q + p.shared_q - 1) / p.shared_q, rows_of_place = g.heads * rows_of_head;
+  int64_t before = 0;  // units of the places before the 64 at hand
   int chunk = 0;       // the first of them
   int32_t len_l = 0;
-  int64_t upto = 0;    // tiles up to and with the lane's place
+  int64_t upto = 0;    // units up to and with the lane's place
   bool there, bad;
   auto look = [&]() {
     len_l = place_len(g, a, p, chunk + lane, there, bad);
-    upto = before + wave_scan(there ? (int64_t)tiles_of(len_l) : 0);
+    upto = before + wave_scan(there ? (int64_t)tiles_of(len_l) * rows_of_place : 0);
   };
   for (;;) {
     look();
-    places += __builtin_popcountll(__builtin_amdgcn_ballot_w64(there));
     if (bad && blockIdx.x == 0) set_status(status, SKV_ERR_ARG);
     if (chunk + 64 >= p.n) break;
     before = lane_of(upto, 63);
     chunk += 64;
   }
-  const int64_t all = lane_of(upto, 63);
-  const bool team = all >= kTeamUnits * places;
-  const int row_tiles = team ? p.shared_q : 1;                               // tiles of query heads in a row
-  const int rows_of_head = (p.tiles_q + row_tiles - 1) / row_tiles, rows_of_place = g.heads * rows_of_head;
-  const int64_t units = all * rows_of_place;
-  const int64_t most = team ? p.blocks : (int64_t)p.blocks * kTeam;
-  const int64_t fit = units / (team ? kMinUnits * kTeam : kMinUnits);
-  const int64_t active = fit < 1 ? 1 : (fit < most ? fit : most);
-  const int64_t me = team ? blockIdx.x : (int64_t)wave * p.blocks + blockIdx.x;
-  int4 *const note = &p.split[(int64_t)wave * p.blocks + blockIdx.x];
-  int4 split = make_int4(0, 0, 0, 0);
-  if (units == 0 || me >= active) {
-    if (lane == 0) *note = split;
+  const int64_t units = lane_of(upto, 63);
+  const int64_t fit = units / kMinUnits;
+  const int64_t active = fit < 1 ? 1 : (fit < p.blocks ? fit : p.blocks);
+  if (units == 0 || (int64_t)blockIdx.x >= active) {
+    if (threadIdx.x == 0) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
-  int64_t u = first_unit(me, units, active);
-  const int64_t end = first_unit(me + 1, units, active);
+  const int64_t run = first_unit(blockIdx.x, units, active), run_end = first_unit(blockIdx.x + 1, units, active);
+  // this wave's part of the run, and its tile of each row's query heads
+  const int parts = NW / p.shared_q, my_part = wave / p.shared_q, my_tile = wave & (p.shared_q - 1);
+  int64_t u = run + (run_end - run) * my_part / parts;
+  const int64_t begun = u, end = run + (run_end - run) * (my_part + 1) / parts;
+  if (my_tile == 0 && lane < 2) rows[my_part][lane].tiles = 0;
   if (chunk > 0) {
     before = 0;
     chunk = 0;
     look();
   }
-  const int64_t begun = u;
   while (u < end) {
     // the place of unit u: the first whose units reach beyond it
-    uint64_t beyond = __builtin_amdgcn_ballot_w64(upto * rows_of_place > u);
+    uint64_t beyond = __builtin_amdgcn_ballot_w64(upto > u);
     while (beyond == 0 && chunk + 64 < p.n) {
       before = lane_of(upto, 63);
       chunk += 64;
       look();
-      beyond = __builtin_amdgcn_ballot_w64(upto * rows_of_place > u);
+      beyond = __builtin_amdgcn_ballot_w64(upto > u);
     }
     if (beyond == 0) break;  // only where lengths change under the call
     const int at = __builtin_ctzll(beyond);
     const int i = chunk + at;
     const int32_t len = __builtin_amdgcn_readlane(len_l, at);
     const int32_t tiles = tiles_of(len);
-    const int64_t in_place = u - (lane_of(upto, at) - tiles) * rows_of_place;
+    const int64_t in_place = u - (lane_of(upto, at) - (int64_t)tiles * rows_of_place);
     const int r = (int)(in_place / tiles);             // (KV head, its row)
     const int32_t ta = (int32_t)(in_place - (int64_t)r * tiles);
     const int32_t tb = (int32_t)min((int64_t)tiles, ta + (end - u));
-    const int h = r / rows_of_head, q0 = (r - h * rows_of_head) * row_tiles * kHeads;  // first query head of the row
+    const int h = r / rows_of_head, q0 = (r - h * rows_of_head) * p.shared_q * kHeads;  // first query head of the row
+    const int32_t row_at = (int32_t)((int64_t)i * p.q_heads + (int64_t)h * p.group + q0);
+    const int row_heads = min(p.shared_q * kHeads, p.group - q0);
+    const int heads = min(kHeads, row_heads - my_tile * kHeads);  // of the wave's tile; none where the row has no such
     const bool whole = ta == 0 && tb == tiles;
-    const int slot = u == begun ? 0 : 1;
-    const int row_heads = min(row_tiles * kHeads, p.group - q0);
-    const int64_t row_at = (int64_t)i * p.q_heads + (int64_t)h * p.group + q0;
-    if (ta == 0 && !whole)
-      split = split_of(worker_with(u + tiles - 1, units, active) - me + 1, team, slot, (int32_t)row_at, row_heads, h);
+    const int slot = u == begun && !whole ? 0 : 1;
+    if (!whole && my_tile == 0 && lane == 0) rows[my_part][slot] = Row{u - ta, tiles, row_at, row_heads, h};
     u += tb - ta;
 
-    // this wave's tile of query heads, and its part of the tokens
-    const int my_tile = team ? wave & (p.shared_q - 1) : 0;
-    const int parts = team ? kTeam / p.shared_q : 1, part = team ? wave / p.shared_q : 0;
-    const int32_t wa = ta + (int32_t)((int64_t)(tb - ta) * part / parts);
-    const int32_t wb = ta + (int32_t)((int64_t)(tb - ta) * (part + 1) / parts);
-    const int heads = min(kHeads, row_heads - my_tile * kHeads);  // none where it has no tile
     float m = -INFINITY, l = 0.0f;
     f32x4 o[NV * CW];
 #pragma unroll
     for (int k = 0; k < NV * CW; ++k) o[k] = f32x4{0, 0, 0, 0};
 
-    if (len > 0 && heads > 0 && wa < wb) {
+    if (len > 0 && heads > 0) {
       const int32_t s = p.seqs[i];
       bf16x8 qf[KB];
       const uint16_t *qp = p.q + (int64_t)i * p.q_stride + (int64_t)(h * p.group + q0 + my_tile * kHeads + hd) * D;
@@ -402,8 +390,8 @@ __global__ __launch_bounds__(64 * kTeam, blocks_per_cu(D)) void k_attend(PGeo g,
 
       Ids ids;
       ids.row = a.table + (int64_t)s * g.max_pages;
-      ids.first = wa * kTile >> g.log2P;
-      ids.last = (int32_t)((min((uint32_t)wb * kTile, (uint32_t)len) - 1) >> g.log2P);
+      ids.first = ta * kTile >> g.log2P;
+      ids.last = (int32_t)((min((uint32_t)tb * kTile, (uint32_t)len) - 1) >> g.log2P);
       ids.n_pages = g.n_pages;
       ids.fetch(status);
       const uint8_t *kbase = static_cast<const uint8_t *>(a.pool) + (int64_t)layer * g.n_pages * g.page_bytes + (int64_t)h * g.P * row;
@@ -416,9 +404,9 @@ __global__ __launch_bounds__(64 * kTeam, blocks_per_cu(D)) void k_attend(PGeo g,
       };
 
       K keys;
-      const uint8_t *b0 = half(wa, 0), *b1 = half(wa, 1);
+      const uint8_t *b0 = half(ta, 0), *b1 = half(ta, 1);
       keys.load(b0, b1);
-      for (int32_t t = wa; t < wb; ++t) {
+      for (int32_t t = ta; t < tb; ++t) {
         const int left = len - t * kTile;  // tokens from here on
         V vals;
         vals.load(b0 + to_v, b1 + to_v, 0);
@@ -428,7 +416,7 @@ __global__ __launch_bounds__(64 * kTeam, blocks_per_cu(D)) void k_attend(PGeo g,
         for (int j = 0; j < KB; ++j)
 #pragma unroll
           for (int b = 0; b < 2; ++b) z[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(keys.operand(b, j), qf[j], z[b], 0, 0, 0);
-        if (t + 1 < wb) {
+        if (t + 1 < tb) {
           b0 = half(t + 1, 0);
           b1 = half(t + 1, 1);
           keys.load(b0, b1);
@@ -479,8 +467,8 @@ __global__ __launch_bounds__(64 * kTeam, blocks_per_cu(D)) void k_attend(PGeo g,
       l = sum_over_rows(l);
     }
 
-    // To LDS: a lane has channels 128 c + CW (4 grp + x) + k of its head in
-    // o[c CW + k][x].  Where waves share the row, those of a tile are joined there.
+    // To LDS: a lane has channels 128 c + CW (4 grp + x) + k of its head in o[c CW + k][x].
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (hd < heads) {
 #pragma unroll
       for (int c = 0; c < NV; ++c)
@@ -489,93 +477,111 @@ __global__ __launch_bounds__(64 * kTeam, blocks_per_cu(D)) void k_attend(PGeo g,
 #pragma unroll
           for (int k = 0; k < CW; ++k) {
             const int ch = 128 * c + CW * (4 * grp + x) + k;
-            if (D >= 16 || ch < D) os[wave][hd][ch] = o[c * CW + k][x];
+            if (D >= 16 || ch < D) os[wave][slot][hd][ch] = o[c * CW + k][x];
           }
       if (grp == 0) {
-        sm[wave][hd] = m;
-        sl[wave][hd] = l;
+        sm[wave][slot][hd] = m;
+        sl[wave][slot][hd] = l;
       }
     }
-    if (team) __syncthreads();
-    else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const int kept = kept_heads(p.kept, team);
-    float *pp = p.part + (me * 2 + slot) * slot_floats(kept, D);
-    const float vs = p.v_scale ? p.v_scale[h] : 1.0f;
-    for (int v = (team ? (int)threadIdx.x : lane) * 4; v < row_heads * D; v += (team ? kTeam * 64 : 64) * 4) {
-      const int hh = v / D, ch = v - hh * D;
-      const int w0 = team ? hh / kHeads : wave, hw = hh & (kHeads - 1);
-      float mx = sm[w0][hw];
-      for (int k = 1; k < parts; ++k) mx = __builtin_fmaxf(mx, sm[w0 + k * p.shared_q][hw]);
-      const float mb = base_of(mx);
-      float ls = 0.0f;
-      f32x4 ov = {0, 0, 0, 0};
-      for (int k = 0; k < parts; ++k) {
-        const int w = w0 + k * p.shared_q;
-        const float e = __builtin_amdgcn_exp2f(sm[w][hw] - mb);
-        ls = __builtin_fmaf(e, sl[w][hw], ls);
-        const f32x4 x = *reinterpret_cast<const f32x4 *>(&os[w][hw][ch]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ov[c] = __builtin_fmaf(e, x[c], ov[c]);
+    if (whole) {  // written from there, in order
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const float vs = p.v_scale ? p.v_scale[h] : 1.0f;
+      for (int v = lane * 4; v < heads * D; v += 256) {
+        const int hh = v / D, ch = v - hh * D;
+        const int64_t q = row_at + my_tile * kHeads + hh;
+        const float mx = sm[wave][1][hh], ls = sl[wave][1][hh], f = ls == 0.0f ? 0.0f : vs / ls;
+        const f32x4 x = *reinterpret_cast<const f32x4 *>(&os[wave][1][hh][ch]);
+        *reinterpret_cast<uint2 *>(p.out + q * D + ch) = make_uint2(pack_bf16(x[0] * f, x[1] * f), pack_bf16(x[2] * f, x[3] * f));
+        if (p.lse && ch == 0) p.lse[q] = ls == 0.0f ? -INFINITY : (mx + __builtin_log2f(ls)) * kLn2;
       }
-      if (whole) {
-        const float f = ls == 0.0f ? 0.0f : vs / ls;
-        *reinterpret_cast<uint2 *>(p.out + (row_at + hh) * D + ch) = make_uint2(pack_bf16(ov[0] * f, ov[1] * f), pack_bf16(ov[2] * f, ov[3] * f));
-        if (p.lse && ch == 0) p.lse[row_at + hh] = ls == 0.0f ? -INFINITY : (mx + __builtin_log2f(ls)) * kLn2;
-      } else {
-        *reinterpret_cast<f32x4 *>(pp + v) = ov;
-        if (ch == 0) {
-          pp[kept * D + hh] = mx;
-          pp[kept * (D + 1) + hh] = ls;
+    }
+  }
+  __syncthreads();
+
+  // rows that span waves: each is a run of the parts' first and last rows
+  int4 split = make_int4(0, 0, 0, 0);
+  const Row *const flat = &rows[0][0];
+  for (int k0 = 0; k0 < 2 * parts;) {
+    const Row r = flat[k0];
+    int k1 = k0 + 1;
+    while (r.tiles > 0 && k1 < 2 * parts && (flat[k1].tiles == 0 || flat[k1].u0 == r.u0)) ++k1;
+    if (r.tiles > 0) {
+      const bool begins = r.u0 >= run, ends = r.u0 + r.tiles <= run_end;
+      const int place = r.u0 <= run ? 0 : 1;
+      if (begins && !ends)
+        split = make_int4((int)(block_with(r.u0 + r.tiles - 1, units, active) - blockIdx.x + 1) << 1 | place, r.at, r.heads, r.h);
+      float *pp = p.part + ((int64_t)blockIdx.x * 2 + place) * p.slot;
+      const float vs = p.v_scale ? p.v_scale[r.h] : 1.0f;
+      for (int v = threadIdx.x * 4; v < r.heads * D; v += NW * 256) {
+        const int hh = v / D, ch = v - hh * D, tile = hh / kHeads, hw = hh & (kHeads - 1);
+        float mx = -INFINITY;
+        for (int k = k0; k < k1; ++k)
+          if (flat[k].tiles) mx = __builtin_fmaxf(mx, sm[(k >> 1) * p.shared_q + tile][k & 1][hw]);
+        const float mb = base_of(mx);
+        float ls = 0.0f;
+        f32x4 ov = {0, 0, 0, 0};
+        for (int k = k0; k < k1; ++k) {
+          if (flat[k].tiles == 0) continue;
+          const int w = (k >> 1) * p.shared_q + tile;
+          const float e = __builtin_amdgcn_exp2f(sm[w][k & 1][hw] - mb);
+          ls = __builtin_fmaf(e, sl[w][k & 1][hw], ls);
+          const f32x4 x = *reinterpret_cast<const f32x4 *>(&os[w][k & 1][hw][ch]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) ov[c] = __builtin_fmaf(e, x[c], ov[c]);
+        }
+        if (begins && ends) {
+          const float f = ls == 0.0f ? 0.0f : vs / ls;
+          *reinterpret_cast<uint2 *>(p.out + (int64_t)(r.at + hh) * D + ch) = make_uint2(pack_bf16(ov[0] * f, ov[1] * f), pack_bf16(ov[2] * f, ov[3] * f));
+          if (p.lse && ch == 0) p.lse[r.at + hh] = ls == 0.0f ? -INFINITY : (mx + __builtin_log2f(ls)) * kLn2;
+        } else {
+          *reinterpret_cast<f32x4 *>(pp + v) = ov;
+          if (ch == 0) {
+            pp[p.kept * D + hh] = mx;
+            pp[p.kept * (D + 1) + hh] = ls;
+          }
         }
       }
     }
-    if (team) __syncthreads();
-    else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    k0 = k1;
   }
-  // of a workgroup the first wave's word says it all
-  if (lane == 0) *note = team && wave > 0 ? make_int4(0, 0, 0, 0) : split;
+  if (threadIdx.x == 0) p.split[blockIdx.x] = split;
 }
 
 // ---- the join ----
-// out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w over the workers w that a
-// row spans.  A workgroup takes 256 of the row's values, four to a lane; each of its
-// waves runs through every fourth partial sum with a running maximum as the main
-// kernel does, all loads of a round in flight at once, and the four are joined
-// in LDS.  Rows of single waves have few partial sums, and a wave each.
-// Workgroups of workers that leave no such row end after one load.
+// out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w over the workgroups w that
+// a row spans.  A workgroup here takes 256 of the row's values, four to a lane;
+// each of its waves runs through every fourth partial sum with a running maximum as
+// the main kernel does, all loads of a round in flight at once, and the four are
+// joined in LDS.  Where no such row begins it ends after one load.
 constexpr int kJoin = 256;
 
 __global__ __launch_bounds__(kJoin) void k_attend_join(PGeo g, AttendArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int4 first = p.split[blockIdx.x], own = p.split[(int64_t)wave * p.blocks + blockIdx.x];
-  const bool team = first.x & 2;
-  const int4 sp = team ? first : own;
-  const int parts = sp.x >> 2;
+  const int4 sp = p.split[blockIdx.x];
+  const int parts = sp.x >> 1;
   if (parts == 0 || (int)blockIdx.y * 256 >= sp.z * g.D) return;
-  const int64_t w0 = team ? blockIdx.x : (int64_t)wave * p.blocks + blockIdx.x;
-  const int k_first = team ? wave : 0, k_step = team ? 4 : 1;
   const int v = ((int)blockIdx.y * 64 + lane) * 4;  // the lane's first value of the row's heads * D
   const bool in = v < sp.z * g.D;
   const int hd = in ? v / g.D : 0;
-  // partial sum k: the first of worker w0 + k, but for the one that the row begins inside of
-  const int kept = kept_heads(p.kept, team), floats = slot_floats(kept, g.D);
-  auto part = [&](int k) { return p.part + ((w0 + k) * 2 + (k == 0 ? sp.x & 1 : 0)) * floats; };
+  // partial sum k: the first of workgroup w + k, but for the one that the row begins inside of
+  auto part = [&](int k) { return p.part + ((int64_t)(blockIdx.x + k) * 2 + (k == 0 ? sp.x & 1 : 0)) * p.slot; };
   float m = -INFINITY, l = 0.0f;
   f32x4 o = {0, 0, 0, 0};
   constexpr int R = 8;
-  for (int k0 = k_first; k0 < parts; k0 += k_step * R) {
+  for (int k0 = wave; k0 < parts; k0 += 4 * R) {
     float ms[R], ls[R];
     f32x4 os[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int k = k0 + k_step * r;
+      const int k = k0 + 4 * r;
       ms[r] = -INFINITY;
       ls[r] = 0.0f;
       os[r] = f32x4{0, 0, 0, 0};
       if (k < parts && in) {
         const float *pp = part(k);
-        ms[r] = pp[kept * g.D + hd];
-        ls[r] = pp[kept * (g.D + 1) + hd];
+        ms[r] = pp[p.kept * g.D + hd];
+        ls[r] = pp[p.kept * (g.D + 1) + hd];
         os[r] = *reinterpret_cast<const f32x4 *>(pp + v);
       }
     }
@@ -596,25 +602,23 @@ __global__ __launch_bounds__(kJoin) void k_attend_join(PGeo g, AttendArgs p) {
   }
   __shared__ float sm[4][64], sl[4][64];
   __shared__ f32x4 so[4][64];
-  if (team) {
-    sm[wave][lane] = m;
-    sl[wave][lane] = l;
-    so[wave][lane] = o;
-    __syncthreads();
-    if (wave > 0) return;
-    const float mx = __builtin_fmaxf(__builtin_fmaxf(sm[0][lane], sm[1][lane]), __builtin_fmaxf(sm[2][lane], sm[3][lane]));
-    const float mb = base_of(mx);
-    l = 0.0f;
-    o = f32x4{0, 0, 0, 0};
+  sm[wave][lane] = m;
+  sl[wave][lane] = l;
+  so[wave][lane] = o;
+  __syncthreads();
+  if (wave > 0) return;
+  const float mx = __builtin_fmaxf(__builtin_fmaxf(sm[0][lane], sm[1][lane]), __builtin_fmaxf(sm[2][lane], sm[3][lane]));
+  const float mb = base_of(mx);
+  l = 0.0f;
+  o = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float e = __builtin_amdgcn_exp2f(sm[w][lane] - mb);
-      l = __builtin_fmaf(e, sl[w][lane], l);
+  for (int w = 0; w < 4; ++w) {
+    const float e = __builtin_amdgcn_exp2f(sm[w][lane] - mb);
+    l = __builtin_fmaf(e, sl[w][lane], l);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[c] = __builtin_fmaf(e, so[w][lane][c], o[c]);
-    }
-    m = mx;
+    for (int c = 0; c < 4; ++c) o[c] = __builtin_fmaf(e, so[w][lane][c], o[c]);
   }
+  m = mx;
   if (!in) return;
   const float f = l == 0.0f ? 0.0f : (p.v_scale ? p.v_scale[sp.w] : 1.0f) / l;
   const uint2 y = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
@@ -623,7 +627,7 @@ __global__ __launch_bounds__(kJoin) void k_attend_join(PGeo g, AttendArgs p) {
 }
 
 struct Plan {
-  int group, tiles_q, shared_q, kept, blocks;
+  int group, tiles_q, shared_q, kept, blocks, slot;
   int64_t bytes;
 };
 
@@ -631,11 +635,11 @@ Plan attend_plan(const PGeo &g, int64_t q_heads) {
   Plan p;
   p.group = (int)(q_heads / g.heads);
   p.tiles_q = (p.group + kHeads - 1) / kHeads;
-  p.shared_q = p.tiles_q == 1 ? 1 : (p.tiles_q == 2 ? 2 : kTeam);
+  p.shared_q = p.tiles_q == 1 ? 1 : (p.tiles_q == 2 ? 2 : waves_of(g.D));
   p.kept = p.group < kHeads * p.shared_q ? p.group : kHeads * p.shared_q;
   p.blocks = device_cu_count() * blocks_per_cu(g.D);
-  const int64_t shared = slot_floats(p.kept, g.D), alone = (int64_t)kTeam * slot_floats(kept_heads(p.kept, false), g.D);
-  p.bytes = p.blocks * (kTeam * (int64_t)sizeof(int4) + 2 * (int64_t)sizeof(float) * (shared > alone ? shared : alone));
+  p.slot = p.kept * g.D + (2 * p.kept + 3) / 4 * 4;
+  p.bytes = p.blocks * ((int64_t)sizeof(int4) + 2 * (int64_t)sizeof(float) * p.slot);
   return p;
 }
 
@@ -683,16 +687,17 @@ extern "C" int skv_attend(const skv_pages_shape *shape, const skv_pages *pages, 
   p.tiles_q = plan.tiles_q;
   p.shared_q = plan.shared_q;
   p.kept = plan.kept;
+  p.slot = plan.slot;
   p.out = static_cast<uint16_t *>(out);
   p.lse = lse;
   // no more workgroups than the longest sequences that the table holds could use
-  const __int128 units = (__int128)n * g.heads * plan.tiles_q * (((int64_t)g.max_tokens + kTile - 1) / kTile);
+  const __int128 units = (__int128)n * g.heads * plan.tiles_q * (((int64_t)g.max_tokens + kTile - 1) / kTile) / kMinUnits + 1;
   p.blocks = units < plan.blocks ? (int)units : plan.blocks;
   p.split = static_cast<int4 *>(workspace);
-  p.part = reinterpret_cast<float *>(p.split + (int64_t)p.blocks * kTeam);
+  p.part = reinterpret_cast<float *>(p.split + p.blocks);
   const dim3 grid((uint32_t)p.blocks);
   hipStream_t st = static_cast<hipStream_t>(stream);
-#define SKV_ATTEND(F_, D_) case D_: k_attend<F_, D_><<<grid, 64 * kTeam, 0, st>>>(g, *pages, (int)layer, p, status); break
+#define SKV_ATTEND(F_, D_) case D_: k_attend<F_, D_><<<grid, 64 * waves_of(D_), 0, st>>>(g, *pages, (int)layer, p, status); break
 #define SKV_ATTEND_ALL(F_) \
   switch (g.D) { \
     SKV_ATTEND(F_, 8); SKV_ATTEND(F_, 16); SKV_ATTEND(F_, 32); SKV_ATTEND(F_, 64); \
