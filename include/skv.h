@@ -289,7 +289,7 @@ typedef struct skv_pages_shape {
   int64_t page_tokens; /* 16, 32, 64, 128 or 256: a coder chunk is a whole number of pages */
   int64_t n_pages;     /* 1 .. 2^30 */
   int64_t max_seqs;    /* 1 .. 2^20 */
-  int64_t max_pages;   /* entries of a table row; max_pages * page_tokens < 2^31 */
+  int64_t max_pages;   /* entries of a table row; max_pages * page_tokens <= 2^30 */
   int32_t sym_fmt;     /* enum skv_sym_fmt */
   int32_t reserved;    /* 0 */
 } skv_pages_shape;

@@ -93,13 +93,14 @@ __device__ __forceinline__ int32_t place_len(const PGeo &g, const skv_pages &a, 
 
 __device__ __forceinline__ int32_t tiles_of(int32_t len) { return len > 0 ? (int32_t)(((uint32_t)len + kTile - 1) / kTile) : 1; }
 
-__device__ __forceinline__ int64_t wave_scan(int64_t v) {  // inclusive
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t y = __shfl_up(v, d);
-    if (lane >= d) v += y;
-  }
+// inclusive prefix sum over the wave, by row shifts and row broadcasts in the vector unit
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, false);  // row_shr:1
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1 and 3
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2 and 3
   return v;
 }
 
@@ -109,10 +110,24 @@ __device__ __forceinline__ int64_t lane_of(int64_t v, int l) {
   return (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
 }
 
-// runs: workgroup w of `active` has units [first_unit(w), first_unit(w + 1))
-__device__ __forceinline__ int64_t first_unit(int64_t w, int64_t units, int64_t active) { return w * units / active; }
-// the workgroup whose run holds unit u
-__device__ __forceinline__ int64_t block_with(int64_t u, int64_t units, int64_t active) { return ((u + 1) * active - 1) / units; }
+// a / b; of 32 bits where both are, as they are nearly always
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((uint64_t)a | (uint64_t)b) >> 32) return a / b;
+  return (uint32_t)a / (uint32_t)b;
+}
+
+// Runs: of `units` units among `active` workgroups, the first `more` of which
+// have each + 1 and the others `each`.
+struct Runs {
+  int64_t each, more;
+  __device__ __forceinline__ Runs(int64_t units, int64_t active) : each(quotient(units, active)), more(units - each * active) {}
+  __device__ __forceinline__ int64_t first(int64_t w) const { return w * each + min(w, more); }
+  // the workgroup that has unit u
+  __device__ __forceinline__ int64_t of(int64_t u) const {
+    const int64_t big = more * (each + 1);
+    return u < big ? quotient(u, each + 1) : more + quotient(u - big, each);
+  }
+};
 
 // ---- numbers ----
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -309,34 +324,36 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
 
   // units in all, and the place that this workgroup's run begins in
   const int rows_of_head = (p.tiles_q + p.shared_q - 1) / p.shared_q, rows_of_place = g.heads * rows_of_head;
-  int64_t before = 0;  // units of the places before the 64 at hand
+  int64_t before = 0;  // units of 32 tokens in the places before the 64 at hand
   int chunk = 0;       // the first of them
   int32_t len_l = 0;
-  int64_t upto = 0;    // units up to and with the lane's place
+  uint32_t upto = 0;   // of those at hand, up to and with the lane's
   bool there, bad;
   auto look = [&]() {
     len_l = place_len(g, a, p, chunk + lane, there, bad);
-    upto = before + wave_scan(there ? (int64_t)tiles_of(len_l) * rows_of_place : 0);
+    upto = wave_scan(there ? (uint32_t)tiles_of(len_l) : 0);  // 64 lengths of 2^30 at most: 2^31
   };
   for (;;) {
     look();
     if (bad && blockIdx.x == 0) set_status(status, SKV_ERR_ARG);
     if (chunk + 64 >= p.n) break;
-    before = lane_of(upto, 63);
+    before += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
     chunk += 64;
   }
-  const int64_t units = lane_of(upto, 63);
+  const int64_t units = (before + (uint32_t)__builtin_amdgcn_readlane((int)upto, 63)) * rows_of_place;
   const int64_t fit = units / kMinUnits;
   const int64_t active = fit < 1 ? 1 : (fit < p.blocks ? fit : p.blocks);
   if (units == 0 || (int64_t)blockIdx.x >= active) {
     if (threadIdx.x == 0) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
-  const int64_t run = first_unit(blockIdx.x, units, active), run_end = first_unit(blockIdx.x + 1, units, active);
+  const Runs runs(units, active);
+  const int64_t run = runs.first(blockIdx.x), run_end = runs.first(blockIdx.x + 1);
   // this wave's part of the run, and its tile of each row's query heads
-  const int parts = NW / p.shared_q, my_part = wave / p.shared_q, my_tile = wave & (p.shared_q - 1);
-  int64_t u = run + (run_end - run) * my_part / parts;
-  const int64_t begun = u, end = run + (run_end - run) * (my_part + 1) / parts;
+  const int log2q = __builtin_ctz(p.shared_q), parts = NW >> log2q, log2p = __builtin_ctz(parts);
+  const int my_part = __builtin_amdgcn_readfirstlane(wave >> log2q), my_tile = __builtin_amdgcn_readfirstlane(wave & (p.shared_q - 1));
+  int64_t u = run + ((run_end - run) * my_part >> log2p);
+  const int64_t begun = u, end = run + ((run_end - run) * (my_part + 1) >> log2p);
   if (my_tile == 0 && lane < 2) rows[my_part][lane].tiles = 0;
   if (chunk > 0) {
     before = 0;
@@ -345,23 +362,23 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
   }
   while (u < end) {
     // the place of unit u: the first whose units reach beyond it
-    uint64_t beyond = __builtin_amdgcn_ballot_w64(upto > u);
+    uint64_t beyond = __builtin_amdgcn_ballot_w64((before + upto) * rows_of_place > u);
     while (beyond == 0 && chunk + 64 < p.n) {
-      before = lane_of(upto, 63);
+      before += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
       chunk += 64;
       look();
-      beyond = __builtin_amdgcn_ballot_w64(upto > u);
+      beyond = __builtin_amdgcn_ballot_w64((before + upto) * rows_of_place > u);
     }
     if (beyond == 0) break;  // only where lengths change under the call
     const int at = __builtin_ctzll(beyond);
     const int i = chunk + at;
     const int32_t len = __builtin_amdgcn_readlane(len_l, at);
     const int32_t tiles = tiles_of(len);
-    const int64_t in_place = u - (lane_of(upto, at) - (int64_t)tiles * rows_of_place);
-    const int r = (int)(in_place / tiles);             // (KV head, its row)
+    const int64_t in_place = u - (before + (uint32_t)__builtin_amdgcn_readlane((int)upto, at) - tiles) * rows_of_place;
+    const int r = (int)quotient(in_place, tiles);      // (KV head, its row)
     const int32_t ta = (int32_t)(in_place - (int64_t)r * tiles);
     const int32_t tb = (int32_t)min((int64_t)tiles, ta + (end - u));
-    const int h = r / rows_of_head, q0 = (r - h * rows_of_head) * p.shared_q * kHeads;  // first query head of the row
+    const int h = rows_of_head == 1 ? r : r / rows_of_head, q0 = (r - h * rows_of_head) * p.shared_q * kHeads;  // first query head of the row
     const int32_t row_at = (int32_t)((int64_t)i * p.q_heads + (int64_t)h * p.group + q0);
     const int row_heads = min(p.shared_q * kHeads, p.group - q0);
     const int heads = min(kHeads, row_heads - my_tile * kHeads);  // of the wave's tile; none where the row has no such
@@ -499,51 +516,55 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
   }
   __syncthreads();
 
-  // rows that span waves: each is a run of the parts' first and last rows
+  // rows that span waves: parts of one row are neighbours among the parts' first and last rows
   int4 split = make_int4(0, 0, 0, 0);
-  const Row *const flat = &rows[0][0];
-  for (int k0 = 0; k0 < 2 * parts;) {
-    const Row r = flat[k0];
-    int k1 = k0 + 1;
-    while (r.tiles > 0 && k1 < 2 * parts && (flat[k1].tiles == 0 || flat[k1].u0 == r.u0)) ++k1;
-    if (r.tiles > 0) {
-      const bool begins = r.u0 >= run, ends = r.u0 + r.tiles <= run_end;
-      const int place = r.u0 <= run ? 0 : 1;
-      if (begins && !ends)
-        split = make_int4((int)(block_with(r.u0 + r.tiles - 1, units, active) - blockIdx.x + 1) << 1 | place, r.at, r.heads, r.h);
-      float *pp = p.part + ((int64_t)blockIdx.x * 2 + place) * p.slot;
-      const float vs = p.v_scale ? p.v_scale[r.h] : 1.0f;
-      for (int v = threadIdx.x * 4; v < r.heads * D; v += NW * 256) {
-        const int hh = v / D, ch = v - hh * D, tile = hh / kHeads, hw = hh & (kHeads - 1);
-        float mx = -INFINITY;
-        for (int k = k0; k < k1; ++k)
-          if (flat[k].tiles) mx = __builtin_fmaxf(mx, sm[(k >> 1) * p.shared_q + tile][k & 1][hw]);
-        const float mb = base_of(mx);
-        float ls = 0.0f;
-        f32x4 ov = {0, 0, 0, 0};
-        for (int k = k0; k < k1; ++k) {
-          if (flat[k].tiles == 0) continue;
-          const int w = (k >> 1) * p.shared_q + tile;
-          const float e = __builtin_amdgcn_exp2f(sm[w][k & 1][hw] - mb);
+  const Row mine = (&rows[0][0])[lane & (2 * NW - 1)];
+  uint32_t todo = (uint32_t)__builtin_amdgcn_ballot_w64(lane < 2 * parts && mine.tiles > 0);
+  while (todo) {
+    const int k0 = __builtin_ctz(todo);
+    const int64_t u0 = lane_of(mine.u0, k0);
+    const int32_t tiles = __builtin_amdgcn_readlane(mine.tiles, k0), row_at = __builtin_amdgcn_readlane(mine.at, k0);
+    const int row_heads = __builtin_amdgcn_readlane(mine.heads, k0), h = __builtin_amdgcn_readlane(mine.h, k0);
+    const uint32_t of_row = todo & (uint32_t)__builtin_amdgcn_ballot_w64(mine.u0 == u0);
+    todo &= ~of_row;
+    const bool begins = u0 >= run, ends = u0 + tiles <= run_end;
+    const int place = u0 <= run ? 0 : 1;
+    if (begins && !ends) split = make_int4((int)(runs.of(u0 + tiles - 1) - blockIdx.x + 1) << 1 | place, row_at, row_heads, h);
+    float *pp = p.part + ((int64_t)blockIdx.x * 2 + place) * p.slot;
+    const float vs = p.v_scale ? p.v_scale[h] : 1.0f;
+    for (int v = threadIdx.x * 4; v < row_heads * D; v += NW * 256) {
+      const int hh = v / D, ch = v - hh * D, tile = hh / kHeads, hw = hh & (kHeads - 1);
+      float ms[2 * NW], mx = -INFINITY, ls = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 2 * NW; ++k) {
+        ms[k] = of_row >> k & 1 ? sm[((k >> 1) << log2q) + tile][k & 1][hw] : -INFINITY;
+        mx = __builtin_fmaxf(mx, ms[k]);
+      }
+      const float mb = base_of(mx);
+      f32x4 ov = {0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < 2 * NW; ++k) {
+        if (of_row >> k & 1) {
+          const int w = ((k >> 1) << log2q) + tile;
+          const float e = __builtin_amdgcn_exp2f(ms[k] - mb);
           ls = __builtin_fmaf(e, sl[w][k & 1][hw], ls);
           const f32x4 x = *reinterpret_cast<const f32x4 *>(&os[w][k & 1][hw][ch]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) ov[c] = __builtin_fmaf(e, x[c], ov[c]);
         }
-        if (begins && ends) {
-          const float f = ls == 0.0f ? 0.0f : vs / ls;
-          *reinterpret_cast<uint2 *>(p.out + (int64_t)(r.at + hh) * D + ch) = make_uint2(pack_bf16(ov[0] * f, ov[1] * f), pack_bf16(ov[2] * f, ov[3] * f));
-          if (p.lse && ch == 0) p.lse[r.at + hh] = ls == 0.0f ? -INFINITY : (mx + __builtin_log2f(ls)) * kLn2;
-        } else {
-          *reinterpret_cast<f32x4 *>(pp + v) = ov;
-          if (ch == 0) {
-            pp[p.kept * D + hh] = mx;
-            pp[p.kept * (D + 1) + hh] = ls;
-          }
+      }
+      if (begins && ends) {
+        const float f = ls == 0.0f ? 0.0f : vs / ls;
+        *reinterpret_cast<uint2 *>(p.out + (int64_t)(row_at + hh) * D + ch) = make_uint2(pack_bf16(ov[0] * f, ov[1] * f), pack_bf16(ov[2] * f, ov[3] * f));
+        if (p.lse && ch == 0) p.lse[row_at + hh] = ls == 0.0f ? -INFINITY : (mx + __builtin_log2f(ls)) * kLn2;
+      } else {
+        *reinterpret_cast<f32x4 *>(pp + v) = ov;
+        if (ch == 0) {
+          pp[p.kept * D + hh] = mx;
+          pp[p.kept * (D + 1) + hh] = ls;
         }
       }
     }
-    k0 = k1;
   }
   if (threadIdx.x == 0) p.split[blockIdx.x] = split;
 }
@@ -551,12 +572,12 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
 // ---- the join ----
 // out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w over the workgroups w that
 // a row spans.  A workgroup here takes 256 of the row's values, four to a lane;
-// each of its waves runs through every fourth partial sum with a running maximum as
-// the main kernel does, all loads of a round in flight at once, and the four are
+// each of its waves runs through every eighth partial sum with a running maximum as
+// the main kernel does, all loads of a round in flight at once, and the eight are
 // joined in LDS.  Where no such row begins it ends after one load.
-constexpr int kJoin = 256;
+constexpr int kJoinWaves = 8;
 
-__global__ __launch_bounds__(kJoin) void k_attend_join(PGeo g, AttendArgs p) {
+__global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(PGeo g, AttendArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int4 sp = p.split[blockIdx.x];
   const int parts = sp.x >> 1;
@@ -568,13 +589,13 @@ __global__ __launch_bounds__(kJoin) void k_attend_join(PGeo g, AttendArgs p) {
   auto part = [&](int k) { return p.part + ((int64_t)(blockIdx.x + k) * 2 + (k == 0 ? sp.x & 1 : 0)) * p.slot; };
   float m = -INFINITY, l = 0.0f;
   f32x4 o = {0, 0, 0, 0};
-  constexpr int R = 8;
-  for (int k0 = wave; k0 < parts; k0 += 4 * R) {
+  constexpr int R = 16;
+  for (int k0 = wave; k0 < parts; k0 += kJoinWaves * R) {
     float ms[R], ls[R];
     f32x4 os[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int k = k0 + 4 * r;
+      const int k = k0 + kJoinWaves * r;
       ms[r] = -INFINITY;
       ls[r] = 0.0f;
       os[r] = f32x4{0, 0, 0, 0};
@@ -600,25 +621,26 @@ __global__ __launch_bounds__(kJoin) void k_attend_join(PGeo g, AttendArgs p) {
       for (int c = 0; c < 4; ++c) o[c] = __builtin_fmaf(e, os[r][c], o[c]);
     }
   }
-  __shared__ float sm[4][64], sl[4][64];
-  __shared__ f32x4 so[4][64];
+  __shared__ float sm[kJoinWaves][64], sl[kJoinWaves][64];
+  __shared__ f32x4 so[kJoinWaves][64];
   sm[wave][lane] = m;
   sl[wave][lane] = l;
   so[wave][lane] = o;
   __syncthreads();
   if (wave > 0) return;
-  const float mx = __builtin_fmaxf(__builtin_fmaxf(sm[0][lane], sm[1][lane]), __builtin_fmaxf(sm[2][lane], sm[3][lane]));
-  const float mb = base_of(mx);
+  m = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kJoinWaves; ++w) m = __builtin_fmaxf(m, sm[w][lane]);
+  const float mb = base_of(m);
   l = 0.0f;
   o = f32x4{0, 0, 0, 0};
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < kJoinWaves; ++w) {
     const float e = __builtin_amdgcn_exp2f(sm[w][lane] - mb);
     l = __builtin_fmaf(e, sl[w][lane], l);
 #pragma unroll
     for (int c = 0; c < 4; ++c) o[c] = __builtin_fmaf(e, so[w][lane][c], o[c]);
   }
-  m = mx;
   if (!in) return;
   const float f = l == 0.0f ? 0.0f : (p.v_scale ? p.v_scale[sp.w] : 1.0f) / l;
   const uint2 y = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
@@ -711,6 +733,6 @@ extern "C" int skv_attend(const skv_pages_shape *shape, const skv_pages *pages, 
 #undef SKV_ATTEND_ALL
 #undef SKV_ATTEND
   if (hipGetLastError() != hipSuccess) return SKV_ERR_HIP;
-  k_attend_join<<<dim3((uint32_t)p.blocks, (uint32_t)((p.kept * g.D + 255) / 256)), kJoin, 0, st>>>(g, p);
+  k_attend_join<<<dim3((uint32_t)p.blocks, (uint32_t)((p.kept * g.D + 255) / 256)), 64 * kJoinWaves, 0, st>>>(g, p);
   return hipGetLastError() == hipSuccess ? SKV_OK : SKV_ERR_HIP;
 }

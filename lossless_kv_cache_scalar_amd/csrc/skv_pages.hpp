@@ -30,7 +30,7 @@ inline int make_pgeo(const skv_pages_shape *sh, PGeo &g) {
   if (sh->head_dim % 8 != 0 || 512 % sh->head_dim != 0) return SKV_ERR_UNSUPPORTED;
   if (sh->page_tokens < 16 || sh->page_tokens > kChunkTokens || (sh->page_tokens & (sh->page_tokens - 1))) return SKV_ERR_ARG;
   if (sh->n_pages < 1 || sh->n_pages > (1 << 30) || sh->max_seqs < 1 || sh->max_seqs > (1 << 20)) return SKV_ERR_ARG;
-  if (sh->max_pages < 1 || sh->max_pages > (int64_t)INT32_MAX / sh->page_tokens) return SKV_ERR_ARG;
+  if (sh->max_pages < 1 || sh->max_pages > ((int64_t)1 << 30) / sh->page_tokens) return SKV_ERR_ARG;
   g.layers = (int)sh->layers;
   g.heads = (int)sh->kv_heads;
   g.D = (int)sh->head_dim;
