@@ -69,28 +69,26 @@ struct Row {
 };
 
 // ---- the dealing out ----
-// units of list place i; 0 for padding.  An empty sequence has one unit, whose
-// only work is to write its zeros.
-__device__ __forceinline__ int32_t place_len(const PGeo &g, const skv_pages &a, const AttendArgs &p, int i, bool &there,
-                                             bool &bad) {
-  there = false;
+// the sequence of list place i (-1: padding, or none that the cache has) and its length
+struct Place {
+  int32_t s, len;
+};
+__device__ __forceinline__ Place place_of(const PGeo &g, const skv_pages &a, const AttendArgs &p, int i, bool &bad) {
+  Place x = {-1, 0};
   bad = false;
-  if (i >= p.n) return 0;
+  if (i >= p.n) return x;
   const int32_t s = p.seqs[i];
-  if (s < 0) return 0;
-  if (s >= g.max_seqs) {
-    bad = true;
-    return 0;
-  }
-  there = true;
-  const int32_t len = a.lens[s];
-  if (len < 0 || len > g.max_tokens) {
-    bad = true;
-    return 0;
-  }
-  return len;
+  if (s < 0) return x;
+  bad = s >= g.max_seqs;
+  if (bad) return x;
+  x.s = s;
+  x.len = a.lens[s];
+  bad = x.len < 0 || x.len > g.max_tokens;
+  if (bad) x.len = 0;
+  return x;
 }
 
+// units of a row.  An empty sequence has one, whose only work is to write its zeros.
 __device__ __forceinline__ int32_t tiles_of(int32_t len) { return len > 0 ? (int32_t)(((uint32_t)len + kTile - 1) / kTile) : 1; }
 
 // inclusive prefix sum over the wave, by row shifts and row broadcasts in the vector unit
@@ -326,12 +324,12 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
   const int rows_of_head = (p.tiles_q + p.shared_q - 1) / p.shared_q, rows_of_place = g.heads * rows_of_head;
   int64_t before = 0;  // units of 32 tokens in the places before the 64 at hand
   int chunk = 0;       // the first of them
-  int32_t len_l = 0;
+  Place place;         // the lane's
   uint32_t upto = 0;   // of those at hand, up to and with the lane's
-  bool there, bad;
+  bool bad;
   auto look = [&]() {
-    len_l = place_len(g, a, p, chunk + lane, there, bad);
-    upto = wave_scan(there ? (uint32_t)tiles_of(len_l) : 0);  // 64 lengths of 2^30 at most: 2^31
+    place = place_of(g, a, p, chunk + lane, bad);
+    upto = wave_scan(place.s >= 0 ? (uint32_t)tiles_of(place.len) : 0);  // 64 lengths of 2^30 at most: 2^31
   };
   for (;;) {
     look();
@@ -372,7 +370,7 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
     if (beyond == 0) break;  // only where lengths change under the call
     const int at = __builtin_ctzll(beyond);
     const int i = chunk + at;
-    const int32_t len = __builtin_amdgcn_readlane(len_l, at);
+    const int32_t s = __builtin_amdgcn_readlane(place.s, at), len = __builtin_amdgcn_readlane(place.len, at);
     const int32_t tiles = tiles_of(len);
     const int64_t in_place = u - (before + (uint32_t)__builtin_amdgcn_readlane((int)upto, at) - tiles) * rows_of_place;
     const int r = (int)quotient(in_place, tiles);      // (KV head, its row)
@@ -393,7 +391,6 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
     for (int k = 0; k < NV * CW; ++k) o[k] = f32x4{0, 0, 0, 0};
 
     if (len > 0 && heads > 0) {
-      const int32_t s = p.seqs[i];
       bf16x8 qf[KB];
       const uint16_t *qp = p.q + (int64_t)i * p.q_stride + (int64_t)(h * p.group + q0 + my_tile * kHeads + hd) * D;
 #pragma unroll

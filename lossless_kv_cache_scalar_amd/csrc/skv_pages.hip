@@ -16,6 +16,15 @@ namespace {
 constexpr int kPlan = 1024;  // threads of a planning workgroup
 constexpr int kPlanWaves = kPlan / 64;
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// symbols on their way through: past the caches
+template <typename U>
+__device__ __forceinline__ U take(const U *p) { return __builtin_nontemporal_load(p); }
+template <typename U>
+__device__ __forceinline__ void put(U *p, U v) { __builtin_nontemporal_store(v, p); }
+
 // ---- workspace of the planning calls ----
 enum { kHdrOk = 0, kHdrCopies = 1, kHdrLive = 2 };
 
@@ -104,9 +113,9 @@ __device__ __forceinline__ bool failed(const int *err, int32_t *hdr, int32_t *st
 // holders in all, every one of them where r > c, all but the last where r = c.
 // That is what growing them one after another gives (each copy gives up one
 // hold, and the last holder keeps the page), found without an order of events.
-__global__ __launch_bounds__(kPlan) void k_plan_extend(PGeo g, skv_pages a, const int32_t *__restrict__ seqs,
-                                                       const int32_t *__restrict__ n_new, int n, PWork w,
-                                                       int32_t *status) {
+__global__ __launch_bounds__(kPlan) void k_plan_extend_long(PGeo g, skv_pages a, const int32_t *__restrict__ seqs,
+                                                            const int32_t *__restrict__ n_new, int n, PWork w,
+                                                            int32_t *status) {
   __shared__ int err;
   __shared__ int64_t lds[kPlanWaves];
   const int tid = threadIdx.x;
@@ -229,6 +238,142 @@ __global__ __launch_bounds__(kPlan) void k_plan_extend(PGeo g, skv_pages a, cons
   }
 }
 
+// The same for lists of at most kPlan places, a thread to each: what the list
+// says stays in registers, and rows and pages are found again in hash tables in
+// LDS instead of through memory (64 rows: 6 us against 11).
+constexpr int kSlots = 2 * kPlan;
+constexpr int kFree = 2048;  // free pages that LDS holds; more go through the workspace
+
+__device__ __forceinline__ int slot_of(int32_t key) { return (int)(((uint32_t)key * 2654435761u) >> 21) & (kSlots - 1); }
+// the slot of a key that is put in; `had`: it was there
+__device__ __forceinline__ int put_key(int *keys, int32_t key, bool &had) {
+  for (int i = slot_of(key);; i = (i + 1) & (kSlots - 1)) {  // at most half of the slots are ever taken
+    const int old = atomicCAS(&keys[i], -1, key);
+    had = old == key;
+    if (old == -1 || had) return i;
+  }
+}
+
+__global__ __launch_bounds__(kPlan) void k_plan_extend(PGeo g, skv_pages a, const int32_t *__restrict__ seqs,
+                                                       const int32_t *__restrict__ n_new, int n, PWork w,
+                                                       int32_t *status) {
+  __shared__ int err;
+  __shared__ int64_t lds[kPlanWaves];
+  __shared__ int row_key[kSlots], page_key[kSlots], page_cnt[kSlots], page_last[kSlots];
+  __shared__ int32_t off[kPlan], entry0[kPlan];  // by place: pages given out before its own; -1 - (last entry) or first new entry
+  __shared__ int32_t place_row[kPlan];
+  __shared__ int32_t fl[kFree];
+  const int tid = threadIdx.x;
+  const int32_t s = tid < n ? seqs[tid] : -1, add = tid < n ? n_new[tid] : 0;
+  if (tid == 0) err = 0;
+  for (int i = tid; i < kSlots; i += kPlan) {
+    row_key[i] = -1;
+    page_key[i] = -1;
+    page_cnt[i] = 0;
+    page_last[i] = -1;
+  }
+  __syncthreads();
+  int32_t len = 0, page = -1, held = 0;
+  if (s >= 0) {
+    if (s >= g.max_seqs || add < 0) {
+      note(&err, SKV_ERR_ARG);
+    } else {
+      len = a.lens[s];
+      bool had;
+      put_key(row_key, s, had);
+      if (had || len < 0 || len > g.max_tokens) {
+        note(&err, SKV_ERR_ARG);
+      } else if ((int64_t)len + add > g.max_tokens) {
+        note(&err, SKV_ERR_PAGES);
+      } else if (add > 0 && (len & (g.P - 1))) {
+        page = a.table[(int64_t)s * g.max_pages + (len >> g.log2P)];
+        held = good_page(page, g) ? a.refs[page] : 0;
+        if (held < 1) note(&err, SKV_ERR_ARG);
+      }
+    }
+  }
+  if (failed(&err, w.hdr, status)) return;
+  int at = 0;
+  if (page >= 0) {
+    bool had;
+    at = put_key(page_key, page, had);
+    atomicAdd(&page_cnt[at], 1);
+    atomicMax(&page_last[at], tid);
+  }
+  __syncthreads();
+  int64_t need = s >= 0 ? pages_of(len + add, g) - pages_of(len, g) : 0;
+  bool cow = false;
+  if (page >= 0) {
+    if (held < page_cnt[at]) note(&err, SKV_ERR_ARG);  // fewer holds than holders
+    cow = held > page_cnt[at] || page_last[at] != tid;
+    need += cow;
+  }
+  // pages in the upper part, copies in the lower: one sum for both
+  int64_t all;
+  const int64_t before = block_scan(need << 16 | (int64_t)cow, all, lds);
+  const int64_t need_all = all >> 16;
+  const int copies = (int)(all & 0xFFFF);
+  if (need_all > g.n_pages) note(&err, SKV_ERR_PAGES);
+  off[tid] = (int32_t)min(before >> 16, (int64_t)INT32_MAX);  // beyond the pool only where the call fails
+  entry0[tid] = cow ? -1 - (len >> g.log2P) : pages_of(len, g);
+  place_row[tid] = s;
+  if (failed(&err, w.hdr, status)) return;
+  // the lowest free pages, in order
+  const bool in_lds = need_all <= kFree;
+  int64_t found = 0;
+  for (int64_t base = 0; base < g.n_pages && found < need_all; base += (int64_t)kPlan * 4) {
+    const int64_t p = base + (int64_t)tid * 4;
+    int4 r = make_int4(1, 1, 1, 1);
+    if (p + 4 <= g.n_pages) {
+      r = *reinterpret_cast<const int4 *>(a.refs + p);
+    } else {
+      if (p < g.n_pages) r.x = a.refs[p];
+      if (p + 1 < g.n_pages) r.y = a.refs[p + 1];
+      if (p + 2 < g.n_pages) r.z = a.refs[p + 2];
+    }
+    int64_t t;
+    int64_t k = found + block_scan((r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0), t, lds);
+    const int32_t rs[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (rs[c] == 0) {
+        if (!in_lds) agent_store(&w.fl[k], (int32_t)p + c);
+        else if (k < need_all) fl[k] = (int32_t)p + c;
+        ++k;
+      }
+    }
+    found += t;
+  }
+  if (found < need_all) note(&err, SKV_ERR_PAGES);
+  if (failed(&err, w.hdr, status)) return;
+  // from here on the call succeeds: hand the pages out
+  auto freed = [&](int64_t k) { return in_lds ? fl[k] : agent_load(&w.fl[k]); };
+  for (int64_t k = tid; k < need_all; k += kPlan) {
+    int lo = 0, hi = n - 1;  // the last place whose pages begin at or before k
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (off[mid] <= k) lo = mid;
+      else hi = mid - 1;
+    }
+    const int32_t pg = freed(k), e = entry0[lo];
+    const int64_t j = k - off[lo];
+    a.refs[pg] = 1;
+    a.table[(int64_t)place_row[lo] * g.max_pages + (e < 0 ? -1 - e : e) + j] = pg;  // its copy takes the entry before its new ones
+  }
+  if (cow) {
+    const int c = (int)(before & 0xFFFF);
+    atomicAdd(&a.refs[page], -1);
+    w.csrc[c] = page;
+    w.cdst[c] = freed(off[tid]);
+    w.ctok[c] = len & (g.P - 1);
+  }
+  if (s >= 0) a.lens[s] = len + add;
+  if (tid == 0) {
+    w.hdr[kHdrOk] = 1;
+    w.hdr[kHdrCopies] = copies;
+  }
+}
+
 // ---- the list of copies, all layers ----
 // U: the unit of a copy, 16 bytes, or 8 where a token's row has no more.  A
 // workgroup takes pieces of kCopyUnits units of one (copy, layer) at a time.
@@ -250,7 +395,7 @@ __device__ __forceinline__ void copy_pages(const PGeo &g, uint8_t *pool, const P
     U *d = reinterpret_cast<U *>(pool + (l * g.n_pages + w.cdst[c]) * g.page_bytes);
     const int64_t u0 = piece * kCopyUnits;
     for (int64_t u = u0 + threadIdx.x; u < min(u0 + kCopyUnits, lu); u += blockDim.x)
-      if ((uint32_t)(u & (hu - 1)) < keep) d[u] = s[u];
+      if ((uint32_t)(u & (hu - 1)) < keep) put(d + u, take(s + u));
   }
 }
 
@@ -260,9 +405,40 @@ __global__ __launch_bounds__(256) void k_copy_pages(PGeo g, uint8_t *pool, PWork
 }
 
 // ---- fork, truncate ----
+// One workgroup checks the list; where the rows are few it also changes them,
+// a wave to each (32 rows of 64 pages: one launch of 4 us instead of two of 3),
+// else a second launch does, a workgroup to each.
+constexpr int kRowsAtOnce = 64;  // rows of 64 entries, four to a wave
+
+__device__ __forceinline__ void fork_row(const PGeo &g, const skv_pages &a, int32_t s, int32_t d, int32_t len,
+                                         int first, int step, int32_t *status) {
+  const int32_t np = pages_of(len, g);
+  for (int32_t k = first; k < np; k += step) {
+    const int32_t pg = a.table[(int64_t)s * g.max_pages + k];
+    a.table[(int64_t)d * g.max_pages + k] = pg;
+    if (good_page(pg, g)) atomicAdd(&a.refs[pg], 1);
+    else set_status(status, SKV_ERR_ARG);
+  }
+  if (first == 0) a.lens[d] = len;
+}
+
+// `len` was read by all of the row's threads before any writes the new one
+__device__ __forceinline__ void truncate_row(const PGeo &g, const skv_pages &a, int32_t s, int32_t len, int32_t to,
+                                             int first, int step, int32_t *status) {
+  const int32_t np = pages_of(len, g);
+  for (int32_t k = pages_of(to, g) + first; k < np; k += step) {
+    int32_t *entry = &a.table[(int64_t)s * g.max_pages + k];
+    const int32_t pg = *entry;
+    *entry = -1;
+    if (good_page(pg, g)) atomicSub(&a.refs[pg], 1);
+    else set_status(status, SKV_ERR_ARG);
+  }
+  if (first == 0) a.lens[s] = to;
+}
+
 __global__ __launch_bounds__(kPlan) void k_check_fork(PGeo g, skv_pages a, const int32_t *__restrict__ src,
                                                       const int32_t *__restrict__ dst,
-                                                      const int32_t *__restrict__ n_tokens, int n, PWork w,
+                                                      const int32_t *__restrict__ n_tokens, int n, int apply, PWork w,
                                                       int32_t *status) {
   __shared__ int err;
   if (threadIdx.x == 0) err = 0;
@@ -286,28 +462,22 @@ __global__ __launch_bounds__(kPlan) void k_check_fork(PGeo g, skv_pages a, const
       note(&err, SKV_ERR_ARG);
   if (failed(&err, w.hdr, status)) return;
   if (threadIdx.x == 0) w.hdr[kHdrOk] = 1;
+  if (!apply) return;
+  for (int i = threadIdx.x >> 6; i < n; i += kPlanWaves)
+    if (src[i] >= 0 && dst[i] >= 0)
+      fork_row(g, a, src[i], dst[i], n_tokens ? n_tokens[i] : a.lens[src[i]], threadIdx.x & 63, 64, status);
 }
 
 __global__ __launch_bounds__(256) void k_fork(PGeo g, skv_pages a, const int32_t *__restrict__ src,
                                               const int32_t *__restrict__ dst, const int32_t *__restrict__ n_tokens,
                                               PWork w, int32_t *status) {
-  if (w.hdr[kHdrOk] == 0) return;
   const int i = blockIdx.x;
-  const int32_t s = src[i], d = dst[i];
-  if (s < 0 || d < 0) return;
-  const int32_t len = n_tokens ? n_tokens[i] : a.lens[s];
-  const int32_t np = pages_of(len, g);
-  for (int32_t k = threadIdx.x; k < np; k += blockDim.x) {
-    const int32_t pg = a.table[(int64_t)s * g.max_pages + k];
-    a.table[(int64_t)d * g.max_pages + k] = pg;
-    if (good_page(pg, g)) atomicAdd(&a.refs[pg], 1);
-    else set_status(status, SKV_ERR_ARG);
-  }
-  if (threadIdx.x == 0) a.lens[d] = len;
+  if (w.hdr[kHdrOk] == 0 || src[i] < 0 || dst[i] < 0) return;
+  fork_row(g, a, src[i], dst[i], n_tokens ? n_tokens[i] : a.lens[src[i]], threadIdx.x, blockDim.x, status);
 }
 
 __global__ __launch_bounds__(kPlan) void k_check_truncate(PGeo g, skv_pages a, const int32_t *__restrict__ seqs,
-                                                          const int32_t *__restrict__ keep, int n, PWork w,
+                                                          const int32_t *__restrict__ keep, int n, int apply, PWork w,
                                                           int32_t *status) {
   __shared__ int err;
   if (threadIdx.x == 0) err = 0;
@@ -325,25 +495,18 @@ __global__ __launch_bounds__(kPlan) void k_check_truncate(PGeo g, skv_pages a, c
     if (seqs[i] >= 0 && agent_load(&w.mark[seqs[i]]) != i) note(&err, SKV_ERR_ARG);
   if (failed(&err, w.hdr, status)) return;
   if (threadIdx.x == 0) w.hdr[kHdrOk] = 1;
+  if (!apply) return;
+  for (int i = threadIdx.x >> 6; i < n; i += kPlanWaves)
+    if (seqs[i] >= 0) truncate_row(g, a, seqs[i], a.lens[seqs[i]], keep ? keep[i] : 0, threadIdx.x & 63, 64, status);
 }
 
 __global__ __launch_bounds__(256) void k_truncate(PGeo g, skv_pages a, const int32_t *__restrict__ seqs,
                                                   const int32_t *__restrict__ keep, PWork w, int32_t *status) {
-  if (w.hdr[kHdrOk] == 0) return;
   const int i = blockIdx.x;
-  const int32_t s = seqs[i];
-  if (s < 0) return;
-  const int32_t len = a.lens[s], to = keep ? keep[i] : 0;
-  const int32_t np = pages_of(len, g);
-  for (int32_t k = pages_of(to, g) + threadIdx.x; k < np; k += blockDim.x) {
-    int32_t *entry = &a.table[(int64_t)s * g.max_pages + k];
-    const int32_t pg = *entry;
-    *entry = -1;
-    if (good_page(pg, g)) atomicSub(&a.refs[pg], 1);
-    else set_status(status, SKV_ERR_ARG);
-  }
+  if (w.hdr[kHdrOk] == 0 || seqs[i] < 0) return;
+  const int32_t len = a.lens[seqs[i]];
   __syncthreads();
-  if (threadIdx.x == 0) a.lens[s] = to;
+  truncate_row(g, a, seqs[i], len, keep ? keep[i] : 0, threadIdx.x, blockDim.x, status);
 }
 
 // ---- compact ----
@@ -425,48 +588,69 @@ __device__ __forceinline__ uint32_t e4m3_two(uint32_t w, float scale) {
   return e4m3_pair(__uint_as_float(w << 16) / scale, __uint_as_float(w & 0xFFFF0000u) / scale);
 }
 
+//
+// A workgroup takes `tokens` tokens, 256 units of each at a time.  Where a token
+// goes is a chain of four loads (row, length, table, holders), which one thread
+// per token goes through while the symbols of all of them are on their way.
+constexpr int kStoreTokens = 8;
+
 template <int E4M3>
 __global__ __launch_bounds__(256) void k_store(PGeo g, skv_pages a, int layer, const uint16_t *__restrict__ k,
                                                int64_t ks, const uint16_t *__restrict__ v, int64_t vs,
                                                const float *__restrict__ k_scale, const float *__restrict__ v_scale,
                                                const int32_t *__restrict__ seqs, const int32_t *__restrict__ pos,
-                                               int64_t n, int per_block, int32_t *status) {
-  const int half = g.heads * g.D / 8, units = 2 * half;  // threads of a token
-  const int parts = per_block > 1 ? 1 : (units + 255) / 256;
-  int64_t t;
-  int u;
-  if (per_block > 1) {
-    const int j = threadIdx.x / units;
-    if (j >= per_block) return;
-    t = (int64_t)blockIdx.x * per_block + j;
-    u = threadIdx.x - j * units;
-  } else {
-    t = blockIdx.x / parts;
-    u = (int)(blockIdx.x % parts) * 256 + threadIdx.x;
-  }
-  if (t >= n || u >= units) return;
-  const int32_t s = seqs[t];
-  if (s < 0) return;
-  if (s >= g.max_seqs) { set_status(status, SKV_ERR_ARG); return; }
-  const int32_t p = pos[t], len = a.lens[s];
-  if (p < 0 || p >= len || len > g.max_tokens) { set_status(status, SKV_ERR_ARG); return; }
-  const int32_t pg = a.table[(int64_t)s * g.max_pages + (p >> g.log2P)];
-  if (!good_page(pg, g) || a.refs[pg] != 1) { set_status(status, SKV_ERR_ARG); return; }
+                                               int64_t n, int tokens, int parts, int32_t *status) {
+  __shared__ int64_t to[256];  // a token's place in the pool; -1: none
+  const int half = g.heads * g.D / 8, units = 2 * half;  // units of a token
+  const int at_once = parts > 1 ? 1 : 256 / units;       // tokens that the workgroup's threads cover
+  const int64_t t0 = (int64_t)(blockIdx.x / (uint32_t)parts) * tokens;
+  const int j = parts > 1 ? 0 : threadIdx.x / units;
+  const int u = parts > 1 ? (int)(blockIdx.x % (uint32_t)parts) * 256 + threadIdx.x : threadIdx.x - j * units;
+  const bool in = u < units && j < at_once;
   const int which = u >= half, hu = which ? u - half : u;
-  const uint16_t *row = which ? v + t * vs : k + t * ks;
-  const uint4 x = *reinterpret_cast<const uint4 *>(row + hu * 8);
+  u32x4 x[kStoreTokens];
+#pragma unroll
+  for (int r = 0; r < kStoreTokens; ++r) {
+    const int64_t t = t0 + r * at_once + j;
+    if (in && r * at_once + j < tokens && t < n) x[r] = take(reinterpret_cast<const u32x4 *>((which ? v + t * vs : k + t * ks) + hu * 8));
+  }
+  if (threadIdx.x < tokens) {
+    const int64_t t = t0 + threadIdx.x;
+    int64_t at = -1;
+    const int32_t s = t < n ? seqs[t] : -1;
+    if (s >= 0) {
+      bool good = s < g.max_seqs;
+      if (good) {
+        const int32_t p = pos[t], len = a.lens[s];
+        good = p >= 0 && p < len && len <= g.max_tokens;
+        if (good) {
+          const int32_t pg = a.table[(int64_t)s * g.max_pages + (p >> g.log2P)];
+          good = good_page(pg, g) && a.refs[pg] == 1;
+          if (good) at = ((int64_t)layer * g.n_pages + pg) * g.page_bytes + (int64_t)(p & (g.P - 1)) * g.row_bytes;
+        }
+      }
+      if (!good) set_status(status, SKV_ERR_ARG);
+    }
+    to[threadIdx.x] = at;
+  }
+  __syncthreads();
+  if (!in) return;
   const int h = hu * 8 / g.D, c = hu * 8 - h * g.D;
-  uint8_t *out = static_cast<uint8_t *>(a.pool) + ((int64_t)layer * g.n_pages + pg) * g.page_bytes +
-                 ((int64_t)(which * g.heads + h) * g.P + (p & (g.P - 1))) * g.row_bytes + c * (E4M3 ? 1 : 2);
-  if (E4M3) {
-    const float *sp = which ? v_scale : k_scale;
-    const float sc = sp ? sp[h] : 1.0f;
-    uint2 y;
-    y.x = e4m3_two(x.x, sc) | e4m3_two(x.y, sc) << 16;
-    y.y = e4m3_two(x.z, sc) | e4m3_two(x.w, sc) << 16;
-    *reinterpret_cast<uint2 *>(out) = y;
-  } else {
-    *reinterpret_cast<uint4 *>(out) = x;
+  const float *sp = which ? v_scale : k_scale;
+  const float sc = E4M3 && sp ? sp[h] : 1.0f;
+  uint8_t *base = static_cast<uint8_t *>(a.pool) + (int64_t)(which * g.heads + h) * g.P * g.row_bytes + c * (E4M3 ? 1 : 2);
+#pragma unroll
+  for (int r = 0; r < kStoreTokens; ++r) {
+    const int i = r * at_once + j;
+    if (i >= tokens || to[i] < 0) continue;
+    if (E4M3) {
+      u32x2 y;
+      y.x = e4m3_two(x[r].x, sc) | e4m3_two(x[r].y, sc) << 16;
+      y.y = e4m3_two(x[r].z, sc) | e4m3_two(x[r].w, sc) << 16;
+      *reinterpret_cast<u32x2 *>(base + to[i]) = y;
+    } else {
+      *reinterpret_cast<u32x4 *>(base + to[i]) = x[r];
+    }
   }
 }
 
@@ -500,8 +684,8 @@ __global__ __launch_bounds__(256) void k_reorder(PGeo g, skv_pages a, int seq, i
     U *c = reinterpret_cast<U *>(static_cast<uint8_t *>(a.pool) + (l * g.n_pages + pg) * g.page_bytes) +
            (((int64_t)kvh * g.P + (p & (g.P - 1))) << lr) + (u & (ru - 1));
     U *b = xr + (t0 << lr) + u;
-    if (SCATTER) *c = *b;
-    else *b = *c;
+    if (SCATTER) put(c, take(b));
+    else put(b, take(c));
   }
 }
 
@@ -527,6 +711,8 @@ int plan_args(const skv_pages_shape *shape, const skv_pages *pages, const void *
   w = carve_pages(g, workspace);
   return bytes < w.total ? SKV_ERR_ARG : SKV_OK;
 }
+
+bool few_rows(const PGeo &g, int64_t n) { return n * ((g.max_pages + 63) / 64) <= kRowsAtOnce; }
 
 // workgroups of a copy of `pages` pages at most, in all layers
 int64_t copy_blocks(const PGeo &g, int64_t pages) {
@@ -579,12 +765,13 @@ extern "C" int skv_pages_extend(const skv_pages_shape *shape, const skv_pages *p
   if (n == 0) return SKV_OK;
   if (!n_new || !aligned4(n_new)) return SKV_ERR_ARG;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  k_plan_extend<<<1, kPlan, 0, st>>>(g, *pages, seqs, n_new, (int)n, w, status);
+  if (n <= kPlan) k_plan_extend<<<1, kPlan, 0, st>>>(g, *pages, seqs, n_new, (int)n, w, status);
+  else k_plan_extend_long<<<1, kPlan, 0, st>>>(g, *pages, seqs, n_new, (int)n, w, status);
   if ((e = launched()) != SKV_OK) return e;
   const dim3 blocks((uint32_t)copy_blocks(g, n));
   uint8_t *pool = static_cast<uint8_t *>(pages->pool);
-  if (g.row_bytes >= 16) k_copy_pages<uint4><<<blocks, 256, 0, st>>>(g, pool, w);
-  else k_copy_pages<uint2><<<blocks, 256, 0, st>>>(g, pool, w);
+  if (g.row_bytes >= 16) k_copy_pages<u32x4><<<blocks, 256, 0, st>>>(g, pool, w);
+  else k_copy_pages<u32x2><<<blocks, 256, 0, st>>>(g, pool, w);
   return launched();
 }
 
@@ -598,8 +785,9 @@ extern "C" int skv_pages_fork(const skv_pages_shape *shape, const skv_pages *pag
   if (n == 0) return SKV_OK;
   if (!dst || !aligned4(dst) || !aligned4(n_tokens)) return SKV_ERR_ARG;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  k_check_fork<<<1, kPlan, 0, st>>>(g, *pages, src, dst, n_tokens, (int)n, w, status);
-  if ((e = launched()) != SKV_OK) return e;
+  const bool apply = few_rows(g, n);
+  k_check_fork<<<1, kPlan, 0, st>>>(g, *pages, src, dst, n_tokens, (int)n, apply, w, status);
+  if ((e = launched()) != SKV_OK || apply) return e;
   k_fork<<<dim3((uint32_t)n), 256, 0, st>>>(g, *pages, src, dst, n_tokens, w, status);
   return launched();
 }
@@ -614,8 +802,9 @@ extern "C" int skv_pages_truncate(const skv_pages_shape *shape, const skv_pages 
   if (n == 0) return SKV_OK;
   if (!aligned4(keep)) return SKV_ERR_ARG;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  k_check_truncate<<<1, kPlan, 0, st>>>(g, *pages, seqs, keep, (int)n, w, status);
-  if ((e = launched()) != SKV_OK) return e;
+  const bool apply = few_rows(g, n);
+  k_check_truncate<<<1, kPlan, 0, st>>>(g, *pages, seqs, keep, (int)n, apply, w, status);
+  if ((e = launched()) != SKV_OK || apply) return e;
   k_truncate<<<dim3((uint32_t)n), 256, 0, st>>>(g, *pages, seqs, keep, w, status);
   return launched();
 }
@@ -633,8 +822,8 @@ extern "C" int skv_pages_compact(const skv_pages_shape *shape, const skv_pages *
   const int64_t cus = device_cu_count();
   const int rename = (int)(g.max_seqs < cus ? g.max_seqs : cus);
   const dim3 blocks((uint32_t)(rename + copy_blocks(g, (g.n_pages + 1) / 2)));  // at most half the pages move
-  if (g.row_bytes >= 16) k_move_pages<uint4><<<blocks, 256, 0, st>>>(g, *pages, w, rename, status);
-  else k_move_pages<uint2><<<blocks, 256, 0, st>>>(g, *pages, w, rename, status);
+  if (g.row_bytes >= 16) k_move_pages<u32x4><<<blocks, 256, 0, st>>>(g, *pages, w, rename, status);
+  else k_move_pages<u32x2><<<blocks, 256, 0, st>>>(g, *pages, w, rename, status);
   return launched();
 }
 
@@ -654,17 +843,20 @@ extern "C" int skv_pages_store(const skv_pages_shape *shape, const skv_pages *pa
   if (k_stride > INT64_MAX / 2 / n || v_stride > INT64_MAX / 2 / n) return SKV_ERR_ARG;
   if ((k_scale || v_scale) && g.fmt != SKV_SYM_E4M3) return SKV_ERR_ARG;
   if (!aligned4(k_scale) || !aligned4(v_scale)) return SKV_ERR_ARG;
-  const int64_t units = 2 * row / 8;
-  const int per = units <= 128 ? (int)(256 / units) : 1;
-  const int64_t blocks = per > 1 ? (n + per - 1) / per : n * ((units + 255) / 256);
+  // as many tokens to a workgroup, up to eight rounds of its threads, as leave every CU four workgroups
+  const int64_t units = 2 * row / 8, at_once = units <= 256 ? 256 / units : 1, parts = (units + 255) / 256;
+  const int64_t want = n * parts / (device_cu_count() * 4);
+  const int64_t rounds = want / at_once < 1 ? 1 : (want / at_once < kStoreTokens ? want / at_once : kStoreTokens);
+  const int64_t tokens = rounds * at_once < 256 ? rounds * at_once : 256;
+  const int64_t blocks = (n + tokens - 1) / tokens * parts;
   if (blocks > INT32_MAX) return SKV_ERR_ARG;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const dim3 grid((uint32_t)blocks);
   const uint16_t *kp = static_cast<const uint16_t *>(k), *vp = static_cast<const uint16_t *>(v);
   if (g.fmt == SKV_SYM_E4M3)
-    k_store<1><<<grid, 256, 0, st>>>(g, *pages, (int)layer, kp, k_stride, vp, v_stride, k_scale, v_scale, seqs, pos, n, per, status);
+    k_store<1><<<grid, 256, 0, st>>>(g, *pages, (int)layer, kp, k_stride, vp, v_stride, k_scale, v_scale, seqs, pos, n, (int)tokens, (int)parts, status);
   else
-    k_store<0><<<grid, 256, 0, st>>>(g, *pages, (int)layer, kp, k_stride, vp, v_stride, nullptr, nullptr, seqs, pos, n, per, status);
+    k_store<0><<<grid, 256, 0, st>>>(g, *pages, (int)layer, kp, k_stride, vp, v_stride, nullptr, nullptr, seqs, pos, n, (int)tokens, (int)parts, status);
   return launched();
 }
 
@@ -688,11 +880,11 @@ int reorder(const skv_pages_shape *shape, const skv_pages *pages, int64_t seq, i
   const int32_t f = (int32_t)first;
   const int sq = (int)seq;
   if (g.row_bytes >= 16) {
-    if (scatter) k_reorder<uint4, 1><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, xb, status);
-    else k_reorder<uint4, 0><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, xb, status);
+    if (scatter) k_reorder<u32x4, 1><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, xb, status);
+    else k_reorder<u32x4, 0><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, xb, status);
   } else {
-    if (scatter) k_reorder<uint2, 1><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, xb, status);
-    else k_reorder<uint2, 0><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, xb, status);
+    if (scatter) k_reorder<u32x2, 1><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, xb, status);
+    else k_reorder<u32x2, 0><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, xb, status);
   }
   return launched();
 }

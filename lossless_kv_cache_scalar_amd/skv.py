@@ -50,6 +50,10 @@ class SkvPages(C.Structure):
     _fields_ = [("pool", C.c_void_p), ("table", C.c_void_p), ("lens", C.c_void_p), ("refs", C.c_void_p)]
 
 
+# the current stream's address without a Stream object, where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 class SkvError(RuntimeError):
     pass
 
@@ -370,12 +374,12 @@ class Pages:
             table = torch.empty(sh.max_seqs, sh.max_pages, dtype=torch.int32, device=device)
             lens = torch.empty(sh.max_seqs, dtype=torch.int32, device=device)
             refs = torch.empty(sh.n_pages, dtype=torch.int32, device=device)
-        self.shape, self.q_heads = sh, int(q_heads)
+        self.shape, self.q_heads, self._head_dim = sh, int(q_heads), sh.head_dim
         self.pool, self.table, self.lens, self.refs = pool, table, lens, refs
         _fits(pool, pool_bytes, "pool")
         for t, n, what in ((table, sh.max_seqs * sh.max_pages, "table"), (lens, sh.max_seqs, "lens"), (refs, sh.n_pages, "refs")):
             _int32(t, n, what)
-        self.device = pool.device
+        self.device, self._index = pool.device, pool.get_device() if pool.is_cuda else None
         for t, what in ((pool, "pool"), (table, "table"), (lens, "lens"), (refs, "refs")):
             self._here(t, what)
         self.ws_bytes, self.attend_bytes = ws, att
@@ -383,19 +387,22 @@ class Pages:
         self.attend_workspace = torch.empty(att, dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._pages = SkvPages(pool.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr())
-        self._sh, self._pg = C.byref(sh), C.byref(self._pages)
+        self._sh, self._pg, self._lib = C.byref(sh), C.byref(self._pages), load()
+        self._ws, self._aws, self._st = (t.data_ptr() for t in (self.workspace, self.attend_workspace, self.status))
         if new:
             self.reset()
         torch.cuda.current_stream().synchronize()  # the arrays are ready for calls on any stream
 
     def _here(self, t, what: str):
-        if t.device.type != "cuda" or t.device != self.device:
+        if t.get_device() != self._index:  # -1: on the host
             raise SkvError(f"{what}: on {t.device}, not on the cache's GPU")
 
     def _call(self, stream):
         """The stream of a call, once the cache's device is seen to be the current one."""
-        if torch.cuda.current_device() != self.device.index:
+        if torch.cuda.current_device() != self._index:
             raise SkvError(f"the cache is on {self.device}, the current device is cuda:{torch.cuda.current_device()}")
+        if stream is None and _raw_stream is not None:  # a tenth of the time of the Stream object
+            return _raw_stream(self._index)
         return _stream(stream)
 
     def _made_on(self, stream):
@@ -405,22 +412,28 @@ class Pages:
         return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
     def _list(self, t, n, what: str):
-        n = t.numel() if n is None else n
-        _int32(t, n, what)
-        if t.numel() != n:
-            raise SkvError(f"{what}: {t.numel()} entries, {n} wanted")
-        self._here(t, what)
-        return n
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32:
+            raise SkvError(f"{what}: an int32 tensor is wanted")
+        have = t.numel()
+        if n is not None and have != n:
+            raise SkvError(f"{what}: {have} entries, {n} wanted")
+        if not t.is_contiguous():
+            raise SkvError(f"{what}: not contiguous")
+        if t.get_device() != self._index:
+            self._here(t, what)
+        return have
 
     def _rows(self, t, n, heads, what: str):
         """A bf16 [n][heads][head_dim] argument whose rows may lie apart; its row stride in elements."""
-        d = self.shape.head_dim
-        if t.dtype != torch.bfloat16 or t.dim() != 3 or tuple(t.shape) != (n, heads, d):
+        d = self._head_dim
+        if t.dtype is not torch.bfloat16 or t.shape != (n, heads, d):
             raise SkvError(f"{what}: {t.dtype} {list(t.shape)}, bfloat16 {[n, heads, d]} wanted")
-        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        rows, one, unit = t.stride()
+        if unit != 1 or (heads > 1 and one != d):
             raise SkvError(f"{what}: heads and channels are not contiguous")
-        self._here(t, what)
-        return t.stride(0) if n > 1 else heads * d
+        if t.get_device() != self._index:
+            self._here(t, what)
+        return rows if n > 1 else heads * d
 
     def _scales(self, t, what: str):
         if t is None:
@@ -433,7 +446,7 @@ class Pages:
 
     def reset(self, stream=None) -> None:
         """skv_pages_reset: no sequences, every page free."""
-        _check(load().skv_pages_reset(self._sh, self._pg, self._call(stream)), "skv_pages_reset")
+        _check(self._lib.skv_pages_reset(self._sh, self._pg, self._call(stream)), "skv_pages_reset")
 
     def check(self, stream=None) -> None:
         """Wait for the stream, then raise the first error that the device found since the last check."""
@@ -448,8 +461,8 @@ class Pages:
         """skv_pages_extend: room for n_new[i] more tokens of sequence seqs[i]."""
         n = self._list(seqs, None, "seqs")
         self._list(n_new, n, "n_new")
-        _check(load().skv_pages_extend(self._sh, self._pg, seqs.data_ptr(), n_new.data_ptr(), n, self.workspace.data_ptr(),
-                                       self.ws_bytes, self.status.data_ptr(), self._call(stream)), "skv_pages_extend")
+        _check(self._lib.skv_pages_extend(self._sh, self._pg, seqs.data_ptr(), n_new.data_ptr(), n, self._ws,
+                                       self.ws_bytes, self._st, self._call(stream)), "skv_pages_extend")
 
     def fork(self, src, dst, n_tokens=None, stream=None) -> None:
         """skv_pages_fork: row dst[i] shares the pages of row src[i] (of its first n_tokens[i] tokens)."""
@@ -457,8 +470,8 @@ class Pages:
         self._list(dst, n, "dst")
         if n_tokens is not None:
             self._list(n_tokens, n, "n_tokens")
-        _check(load().skv_pages_fork(self._sh, self._pg, src.data_ptr(), dst.data_ptr(), _ptr(n_tokens), n,
-                                     self.workspace.data_ptr(), self.ws_bytes, self.status.data_ptr(),
+        _check(self._lib.skv_pages_fork(self._sh, self._pg, src.data_ptr(), dst.data_ptr(), _ptr(n_tokens), n,
+                                     self._ws, self.ws_bytes, self._st,
                                      self._call(stream)), "skv_pages_fork")
 
     def truncate(self, seqs, keep=None, stream=None) -> None:
@@ -466,8 +479,8 @@ class Pages:
         n = self._list(seqs, None, "seqs")
         if keep is not None:
             self._list(keep, n, "keep")
-        _check(load().skv_pages_truncate(self._sh, self._pg, seqs.data_ptr(), _ptr(keep), n, self.workspace.data_ptr(),
-                                         self.ws_bytes, self.status.data_ptr(), self._call(stream)), "skv_pages_truncate")
+        _check(self._lib.skv_pages_truncate(self._sh, self._pg, seqs.data_ptr(), _ptr(keep), n, self._ws,
+                                         self.ws_bytes, self._st, self._call(stream)), "skv_pages_truncate")
 
     def compact(self, n_live=None, stream=None):
         """skv_pages_compact; the number of pages in use, an int32 tensor of one."""
@@ -475,8 +488,8 @@ class Pages:
             with self._made_on(stream):
                 n_live = torch.empty(1, dtype=torch.int32, device=self.device)
         self._list(n_live, 1, "n_live")
-        _check(load().skv_pages_compact(self._sh, self._pg, n_live.data_ptr(), self.workspace.data_ptr(), self.ws_bytes,
-                                        self.status.data_ptr(), self._call(stream)), "skv_pages_compact")
+        _check(self._lib.skv_pages_compact(self._sh, self._pg, n_live.data_ptr(), self._ws, self.ws_bytes,
+                                        self._st, self._call(stream)), "skv_pages_compact")
         return n_live
 
     def store(self, layer: int, k, v, seqs, pos, k_scale=None, v_scale=None, stream=None) -> None:
@@ -485,9 +498,9 @@ class Pages:
         self._list(pos, n, "pos")
         ks = self._rows(k, n, self.shape.kv_heads, "k")
         vs = self._rows(v, n, self.shape.kv_heads, "v")
-        _check(load().skv_pages_store(self._sh, self._pg, int(layer), k.data_ptr(), ks, v.data_ptr(), vs,
+        _check(self._lib.skv_pages_store(self._sh, self._pg, int(layer), k.data_ptr(), ks, v.data_ptr(), vs,
                                       self._scales(k_scale, "k_scale"), self._scales(v_scale, "v_scale"), seqs.data_ptr(),
-                                      pos.data_ptr(), n, self.status.data_ptr(), self._call(stream)), "skv_pages_store")
+                                      pos.data_ptr(), n, self._st, self._call(stream)), "skv_pages_store")
 
     def coder_shape(self, tokens: int, mu_fmt=MU_BF16, sigma_mode=SIGMA_CHANNEL, phat_mode=PHAT_STATIC) -> SkvShape:
         """The coder's shape of `tokens` tokens of one sequence."""
@@ -507,15 +520,15 @@ class Pages:
                 x = torch.empty(sh.layers, 2, sh.kv_heads, int(tokens), sh.head_dim, device=self.device,
                                 dtype=torch.int16 if sh.sym_fmt == SYM_BF16 else torch.uint8)
         self._tokens(tokens, x)
-        _check(load().skv_pages_gather(self._sh, self._pg, int(seq), int(first), int(tokens), x.data_ptr(),
-                                       self.status.data_ptr(), self._call(stream)), "skv_pages_gather")
+        _check(self._lib.skv_pages_gather(self._sh, self._pg, int(seq), int(first), int(tokens), x.data_ptr(),
+                                       self._st, self._call(stream)), "skv_pages_gather")
         return x
 
     def scatter(self, seq: int, first: int, tokens: int, x, stream=None) -> None:
         """skv_pages_scatter: the way back, from decode()'s output into the sequence's pages."""
         self._tokens(tokens, x)
-        _check(load().skv_pages_scatter(self._sh, self._pg, int(seq), int(first), int(tokens), x.data_ptr(),
-                                        self.status.data_ptr(), self._call(stream)), "skv_pages_scatter")
+        _check(self._lib.skv_pages_scatter(self._sh, self._pg, int(seq), int(first), int(tokens), x.data_ptr(),
+                                        self._st, self._call(stream)), "skv_pages_scatter")
 
     def attend(self, layer: int, q, seqs, scale=None, k_scale=None, v_scale=None, out=None, lse=None, stream=None):
         """skv_attend: attention of q [n][q_heads][head_dim], one token of each sequence in seqs, over the cached
@@ -530,16 +543,16 @@ class Pages:
         elif self._rows(out, n, self.q_heads, "out") != self.q_heads * self.shape.head_dim:
             raise SkvError("out: not contiguous")
         if lse is not None:
-            if lse.dtype != torch.float32 or tuple(lse.shape) != (n, self.q_heads):
-                raise SkvError(f"lse: {lse.dtype} {list(lse.shape)}, float32 {[n, self.q_heads]} wanted")
-            _fits(lse, 4 * n * self.q_heads, "lse")
-            self._here(lse, "lse")
+            if lse.dtype is not torch.float32 or lse.shape != (n, self.q_heads) or not lse.is_contiguous():
+                raise SkvError(f"lse: {lse.dtype} {list(lse.shape)}, contiguous float32 {[n, self.q_heads]} wanted")
+            if lse.get_device() != self._index:
+                self._here(lse, "lse")
         if scale is None:
             scale = self.shape.head_dim ** -0.5
-        _check(load().skv_attend(self._sh, self._pg, int(layer), q.data_ptr(), qs, self.q_heads, float(scale),
+        _check(self._lib.skv_attend(self._sh, self._pg, int(layer), q.data_ptr(), qs, self.q_heads, float(scale),
                                  self._scales(k_scale, "k_scale"), self._scales(v_scale, "v_scale"), seqs.data_ptr(), n,
-                                 out.data_ptr(), _ptr(lse), self.attend_workspace.data_ptr(), self.attend_bytes,
-                                 self.status.data_ptr(), self._call(stream)), "skv_attend")
+                                 out.data_ptr(), _ptr(lse), self._aws, self.attend_bytes,
+                                 self._st, self._call(stream)), "skv_attend")
         return out
 
 
