@@ -379,7 +379,8 @@ __global__ __launch_bounds__(kPlan) void k_plan_extend(PGeo g, skv_pages a, cons
 // workgroup takes pieces of kCopyUnits units of one (copy, layer) at a time.
 constexpr int kCopyUnits = 1024;
 
-template <typename U>
+// STREAM: past the caches, for much data; a page copied for a sequence that grows is soon read again
+template <typename U, int STREAM>
 __device__ __forceinline__ void copy_pages(const PGeo &g, uint8_t *pool, const PWork &w, int64_t first, int64_t step) {
   const int64_t copies = w.hdr[kHdrCopies];
   const uint32_t ru = (uint32_t)g.row_bytes / sizeof(U);             // units of a row
@@ -395,13 +396,16 @@ __device__ __forceinline__ void copy_pages(const PGeo &g, uint8_t *pool, const P
     U *d = reinterpret_cast<U *>(pool + (l * g.n_pages + w.cdst[c]) * g.page_bytes);
     const int64_t u0 = piece * kCopyUnits;
     for (int64_t u = u0 + threadIdx.x; u < min(u0 + kCopyUnits, lu); u += blockDim.x)
-      if ((uint32_t)(u & (hu - 1)) < keep) put(d + u, take(s + u));
+      if ((uint32_t)(u & (hu - 1)) < keep) {
+        if (STREAM) put(d + u, take(s + u));
+        else d[u] = s[u];
+      }
   }
 }
 
 template <typename U>
 __global__ __launch_bounds__(256) void k_copy_pages(PGeo g, uint8_t *pool, PWork w) {
-  copy_pages<U>(g, pool, w, blockIdx.x, gridDim.x);
+  copy_pages<U, 0>(g, pool, w, blockIdx.x, gridDim.x);
 }
 
 // ---- fork, truncate ----
@@ -550,7 +554,7 @@ __global__ __launch_bounds__(kPlan) void k_plan_compact(PGeo g, skv_pages a, int
 template <typename U>
 __global__ __launch_bounds__(256) void k_move_pages(PGeo g, skv_pages a, PWork w, int rename_blocks, int32_t *status) {
   if ((int)blockIdx.x >= rename_blocks) {
-    copy_pages<U>(g, static_cast<uint8_t *>(a.pool), w, blockIdx.x - rename_blocks, gridDim.x - rename_blocks);
+    copy_pages<U, 1>(g, static_cast<uint8_t *>(a.pool), w, blockIdx.x - rename_blocks, gridDim.x - rename_blocks);
     return;
   }
   const int32_t live = w.hdr[kHdrLive];
@@ -584,9 +588,42 @@ __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x, y, 0, false) & 0xFFFFu;
 }
 
-__device__ __forceinline__ uint32_t e4m3_two(uint32_t w, float scale) {
-  return e4m3_pair(__uint_as_float(w << 16) / scale, __uint_as_float(w & 0xFFFF0000u) / scale);
-}
+// Eight bf16 values over a scale, as e4m3.  The quotient is the correctly
+// rounded one (a later rounding to 4 bits would show the difference at ties), but
+// a division costs a dozen instructions.  With y = 1 / s rounded, each step q <-
+// q + (a - q s) y (the remainder exact, by fma) makes q faithful and then
+// correctly rounded (Markstein), so long as nothing overflows, which the limits
+// on s and |a| see to; a remainder that underflows belongs to a quotient far below
+// e4m3's smallest value.  16376 tokens of 2048 values: 31 us with divisions, 23 without.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+struct Scale {
+  float s, y;
+  uint32_t most;  // magnitudes (bf16 patterns) up to this take the short way; 0: none does
+  __device__ __forceinline__ explicit Scale(float scale) : s(scale), y(1.0f / scale) {
+    const float m = __builtin_fabsf(scale);
+    most = m >= 0x1p-60f && m <= 0x1p60f ? __float_as_uint(447.0f * m) >> 16 : 0;
+  }
+  __device__ __forceinline__ float over(float a) const {
+    const float q0 = a * y, q1 = __builtin_fmaf(__builtin_fmaf(-q0, s, a), y, q0);
+    return __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q1, s, a), y, q1), q0);  // -0 / s keeps its sign
+  }
+  __device__ __forceinline__ uint32_t two(uint32_t w, bool quick) const {
+    const float a = __uint_as_float(w << 16), b = __uint_as_float(w & 0xFFFF0000u);
+    if (quick) return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(over(a), over(b), 0, false) & 0xFFFFu;
+    return e4m3_pair(a / s, b / s);
+  }
+  __device__ __forceinline__ u32x2 eight(u32x4 x) const {
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t mag = x[c] & 0x7FFF7FFFu;
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, mag));
+    }
+    const bool quick = __builtin_amdgcn_ballot_w64((uint32_t)max(m.x, m.y) > most || most == 0) == 0;
+    return u32x2{two(x.x, quick) | two(x.y, quick) << 16, two(x.z, quick) | two(x.w, quick) << 16};
+  }
+};
 
 //
 // A workgroup takes `tokens` tokens, 256 units of each at a time.  Where a token
@@ -637,17 +674,14 @@ __global__ __launch_bounds__(256) void k_store(PGeo g, skv_pages a, int layer, c
   if (!in) return;
   const int h = hu * 8 / g.D, c = hu * 8 - h * g.D;
   const float *sp = which ? v_scale : k_scale;
-  const float sc = E4M3 && sp ? sp[h] : 1.0f;
+  const Scale sc(E4M3 && sp ? sp[h] : 1.0f);
   uint8_t *base = static_cast<uint8_t *>(a.pool) + (int64_t)(which * g.heads + h) * g.P * g.row_bytes + c * (E4M3 ? 1 : 2);
 #pragma unroll
   for (int r = 0; r < kStoreTokens; ++r) {
     const int i = r * at_once + j;
     if (i >= tokens || to[i] < 0) continue;
     if (E4M3) {
-      u32x2 y;
-      y.x = e4m3_two(x[r].x, sc) | e4m3_two(x[r].y, sc) << 16;
-      y.y = e4m3_two(x[r].z, sc) | e4m3_two(x[r].w, sc) << 16;
-      *reinterpret_cast<u32x2 *>(base + to[i]) = y;
+      *reinterpret_cast<u32x2 *>(base + to[i]) = sc.eight(x[r]);
     } else {
       *reinterpret_cast<u32x4 *>(base + to[i]) = x[r];
     }
