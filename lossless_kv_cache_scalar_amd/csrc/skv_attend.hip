@@ -28,6 +28,7 @@ namespace {
 constexpr int kTile = 32;    // tokens of a unit
 constexpr int kHeads = 16;   // query heads of a tile
 constexpr int kMinUnits = 4; // units of a workgroup at least
+constexpr float kSplit = 3.0f;
 // waves of a workgroup (LDS holds two partial sums of each) and workgroups of a
 // CU (registers: to 128 channels at most 256 each)
 __host__ __device__ constexpr int waves_of(int D) { return D <= 256 ? 4 : 2; }
@@ -50,7 +51,7 @@ struct AttendArgs {
   int q_heads, group, tiles_q;  // query heads, per KV head, tiles of 16 of them
   int shared_q;                 // tiles of a row, a wave to each: 1, 2 or 4
   int kept;                     // heads of a row at most: min(group, 16 shared_q)
-  int blocks;                   // of the main launch
+  int blocks, cus;              // of the main launch; compute units
   uint16_t *out;
   float *lse;
   int slot;                     // floats of a partial sum: O [kept][D], m [kept], l [kept], rounded up to 4
@@ -323,6 +324,7 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
   // units in all, and the place that this workgroup's run begins in
   const int rows_of_head = (p.tiles_q + p.shared_q - 1) / p.shared_q, rows_of_place = g.heads * rows_of_head;
   int64_t before = 0;  // units of 32 tokens in the places before the 64 at hand
+  int64_t places = 0;
   int chunk = 0;       // the first of them
   Place place;         // the lane's
   uint32_t upto = 0;   // of those at hand, up to and with the lane's
@@ -334,12 +336,18 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
   for (;;) {
     look();
     if (bad && blockIdx.x == 0) set_status(status, SKV_ERR_ARG);
+    places += __builtin_popcountll(__builtin_amdgcn_ballot_w64(place.s >= 0));
     if (chunk + 64 >= p.n) break;
     before += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
     chunk += 64;
   }
   const int64_t units = (before + (uint32_t)__builtin_amdgcn_readlane((int)upto, 63)) * rows_of_place;
-  const int64_t fit = units / kMinUnits;
+  // workgroups that take part: not so many that a row's join costs more than the
+  // split saves.  With w of them a row is read in time ~ units / w and joined in
+  // ~ w / rows; the sum is least where w^2 ~ units * rows.
+  // Above one for each CU it is two for each: three for two CUs take as long as four.
+  int64_t fit = min(units / kMinUnits, (int64_t)(kSplit * __builtin_amdgcn_sqrtf((float)units * (float)(places * rows_of_place))));
+  if (fit > p.cus && fit < p.blocks) fit = p.cus;
   const int64_t active = fit < 1 ? 1 : (fit < p.blocks ? fit : p.blocks);
   if (units == 0 || (int64_t)blockIdx.x >= active) {
     if (threadIdx.x == 0) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -569,25 +577,15 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
 // ---- the join ----
 // out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w over the workgroups w that
 // a row spans.  A workgroup here takes 256 of the row's values, four to a lane;
-// each of its waves runs through every eighth partial sum with a running maximum as
-// the main kernel does, all loads of a round in flight at once, and the eight are
+// each of its waves runs through every fourth partial sum with a running maximum as
+// the main kernel does, all loads of a round in flight at once, and the four are
 // joined in LDS.  Where no such row begins it ends after one load.
-constexpr int kJoinWaves = 8;
+constexpr int kJoinWaves = 4;
 
-__global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(PGeo g, AttendArgs p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int4 sp = p.split[blockIdx.x];
-  const int parts = sp.x >> 1;
-  if (parts == 0 || (int)blockIdx.y * 256 >= sp.z * g.D) return;
-  const int v = ((int)blockIdx.y * 64 + lane) * 4;  // the lane's first value of the row's heads * D
-  const bool in = v < sp.z * g.D;
-  const int hd = in ? v / g.D : 0;
-  // partial sum k: the first of workgroup w + k, but for the one that the row begins inside of
-  auto part = [&](int k) { return p.part + ((int64_t)(blockIdx.x + k) * 2 + (k == 0 ? sp.x & 1 : 0)) * p.slot; };
-  float m = -INFINITY, l = 0.0f;
-  f32x4 o = {0, 0, 0, 0};
-  constexpr int R = 16;
-  for (int k0 = wave; k0 < parts; k0 += kJoinWaves * R) {
+template <int R, typename Part>
+__device__ __forceinline__ void sum_parts(const Part &part, int first, int parts, bool in, int v, int at_m, int at_l, float &m,
+                                          float &l, f32x4 &o) {
+  for (int k0 = first; k0 < parts; k0 += kJoinWaves * R) {
     float ms[R], ls[R];
     f32x4 os[R];
 #pragma unroll
@@ -598,8 +596,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(PGeo g, AttendA
       os[r] = f32x4{0, 0, 0, 0};
       if (k < parts && in) {
         const float *pp = part(k);
-        ms[r] = pp[p.kept * g.D + hd];
-        ls[r] = pp[p.kept * (g.D + 1) + hd];
+        ms[r] = pp[at_m];
+        ls[r] = pp[at_l];
         os[r] = *reinterpret_cast<const f32x4 *>(pp + v);
       }
     }
@@ -618,6 +616,23 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(PGeo g, AttendA
       for (int c = 0; c < 4; ++c) o[c] = __builtin_fmaf(e, os[r][c], o[c]);
     }
   }
+}
+
+__global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(PGeo g, AttendArgs p) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int4 sp = p.split[blockIdx.x];
+  const int parts = sp.x >> 1;
+  if (parts == 0 || (int)blockIdx.y * 256 >= sp.z * g.D) return;
+  const int v = ((int)blockIdx.y * 64 + lane) * 4;  // the lane's first value of the row's heads * D
+  const bool in = v < sp.z * g.D;
+  const int hd = in ? v / g.D : 0;
+  // partial sum k: the first of workgroup w + k, but for the one that the row begins inside of
+  auto part = [&](int k) { return p.part + ((int64_t)(blockIdx.x + k) * 2 + (k == 0 ? sp.x & 1 : 0)) * p.slot; };
+  float m = -INFINITY, l = 0.0f;
+  f32x4 o = {0, 0, 0, 0};
+  const int at_m = p.kept * g.D + hd, at_l = at_m + p.kept;
+  if (parts <= 8 * kJoinWaves) sum_parts<8>(part, wave, parts, in, v, at_m, at_l, m, l, o);
+  else sum_parts<16>(part, wave, parts, in, v, at_m, at_l, m, l, o);
   __shared__ float sm[kJoinWaves][64], sl[kJoinWaves][64];
   __shared__ f32x4 so[kJoinWaves][64];
   sm[wave][lane] = m;
@@ -712,6 +727,7 @@ extern "C" int skv_attend(const skv_pages_shape *shape, const skv_pages *pages, 
   // no more workgroups than the longest sequences that the table holds could use
   const __int128 units = (__int128)n * g.heads * plan.tiles_q * (((int64_t)g.max_tokens + kTile - 1) / kTile) / kMinUnits + 1;
   p.blocks = units < plan.blocks ? (int)units : plan.blocks;
+  p.cus = plan.blocks / blocks_per_cu(g.D);
   p.split = static_cast<int4 *>(workspace);
   p.part = reinterpret_cast<float *>(p.split + p.blocks);
   const dim3 grid((uint32_t)p.blocks);
