@@ -29,10 +29,11 @@ constexpr int kTile = 32;    // tokens of a unit
 constexpr int kHeads = 16;   // query heads of a tile
 constexpr int kMinUnits = 4; // units of a workgroup at least
 constexpr float kSplit = 3.0f;
-// waves of a workgroup (LDS holds two partial sums of each) and workgroups of a
-// CU (registers: to 128 channels at most 256 each)
+// waves of a workgroup (LDS holds two partial sums of each), and of a SIMD
+// (registers: 256 or 512 to a wave)
 __host__ __device__ constexpr int waves_of(int D) { return D <= 256 ? 4 : 2; }
-__host__ __device__ constexpr int blocks_per_cu(int D) { return D <= 128 ? 2 : 1; }
+__host__ __device__ constexpr int waves_per_simd(int fmt, int D) { return D <= 128 || (D == 256 && fmt == SKV_SYM_E4M3) ? 2 : 1; }
+constexpr int kLds = 160 * 1024;  // of a CU
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -60,6 +61,9 @@ struct AttendArgs {
                                 // spans (0: there is none) * 2 + place of the first partial sum, its first place in
                                 // lse, its query heads, its KV head
 };
+
+// floats of a head's row in LDS: sixteen heads' rows then begin in different banks
+__host__ __device__ constexpr int row_floats(int D) { return D + 4; }
 
 // a row of which a wave has a part
 struct Row {
@@ -157,15 +161,19 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
 // ---- a unit's keys and values in registers ----
-// Each is read once, so past the caches: 7.0 TB/s against 6.1 for a plain read of 1 GiB.
-template <typename T>
-__device__ __forceinline__ T streamed(const uint8_t *p) { return __builtin_nontemporal_load(reinterpret_cast<const T *>(p)); }
+// Where each is read once it goes past the caches: 7.0 TB/s against 6.1 for a
+// plain read of 1 GiB.  Several tiles of query heads read the same ones.
+template <int ONCE, typename T>
+__device__ __forceinline__ T fetched(const uint8_t *p) {
+  if (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const T *>(p));
+  return *reinterpret_cast<const T *>(p);
+}
 
 // K, operand A of a 16x16x32 product: lane l holds token l % 16, eight of 32
 // channels by l / 16.  bf16: channels in order; e4m3: a 16-byte load holds the
 // lane's channels of two products (which channels form a product does not
 // matter as long as q takes the same ones).
-template <int FMT, int D>
+template <int FMT, int D, int ONCE>
 struct Keys {
   static constexpr int KB = D < 32 ? 1 : D / 32;                   // products
   static constexpr bool wide = FMT == 0 || D >= 64;                // 16-byte loads
@@ -185,9 +193,9 @@ struct Keys {
       for (int j = 0; j < NL; ++j) {
         if (row >= 4 * bytes || in) {
           if (wide) {
-            r[s][j] = streamed<u32x4>(b + off + j * 64);
+            r[s][j] = fetched<ONCE, u32x4>(b + off + j * 64);
           } else {
-            const u32x2 v = streamed<u32x2>(b + off);
+            const u32x2 v = fetched<ONCE, u32x2>(b + off);
             r[s][j] = u32x4{v.x, v.y, 0, 0};
           }
         } else {
@@ -215,7 +223,7 @@ struct Keys {
 // the lane group holds, 4 g .. 4 g + 3 of either half.  Loaded along the channels,
 // a whole row by 16 lanes; a byte permute turns two tokens' words into
 // two channels' pairs.
-template <int FMT, int D>
+template <int FMT, int D, int ONCE>
 struct Values {
   static constexpr int CW = D < 16 ? 1 : (D < 128 ? D / 16 : 8);
   static constexpr int esz = FMT == 0 ? 2 : 1;
@@ -232,11 +240,11 @@ struct Values {
       const uint8_t *b = (i < 4 ? b0 : b1) + off + (i & 3) * row;
       if (D >= 16 || c < D) {
         if (bytes == 16) {
-          const u32x4 v = streamed<u32x4>(b);
+          const u32x4 v = fetched<ONCE, u32x4>(b);
 #pragma unroll
           for (int k = 0; k < W; ++k) w[i][k] = v[k];
         } else if (bytes == 8) {
-          const u32x2 v = streamed<u32x2>(b);
+          const u32x2 v = fetched<ONCE, u32x2>(b);
           w[i][0] = v.x;
           w[i][W - 1] = v.y;
         } else if (bytes == 4) {
@@ -306,17 +314,21 @@ struct Ids {
   }
 };
 
-template <int FMT, int D>
-__global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(PGeo g, skv_pages a, int layer, AttendArgs p,
-                                                                              int32_t *status) {
-  using K = Keys<FMT, D>;
-  using V = Values<FMT, D>;
+template <int FMT, int D, int ONCE>
+__global__ __launch_bounds__(64 * waves_of(D), waves_per_simd(FMT, D)) void k_attend(PGeo g, skv_pages a, int layer, AttendArgs p,
+                                                                                    int32_t *status) {
+  using K = Keys<FMT, D, ONCE>;
+  using V = Values<FMT, D, ONCE>;
   constexpr int KB = K::KB, CW = V::CW;
   constexpr int NV = D < 128 ? 1 : D / 128;  // chunks of 128 channels
   constexpr int row = K::row;
   constexpr int NW = waves_of(D);
-  constexpr int LD = D + 4;                  // sixteen heads' rows then lie in different banks
-  __shared__ float os[NW][2][kHeads][LD];
+  constexpr int LD = row_floats(D);
+  constexpr bool ahead = D <= 256;           // the next unit's keys are loaded during this one's softmax
+  // [NW][2][tile_heads][LD]: a wave's partial sums
+  extern __shared__ float os[];
+  const int tile_heads = min(p.group, kHeads);
+  auto sum_at = [&](int w, int slot, int hd) { return os + ((w * 2 + slot) * tile_heads + hd) * LD; };
   __shared__ float sm[NW][2][kHeads], sl[NW][2][kHeads];
   __shared__ Row rows[NW][2];                // by part of the run
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = lane & 15, grp = lane >> 4;
@@ -345,9 +357,9 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
   // workgroups that take part: not so many that a row's join costs more than the
   // split saves.  With w of them a row is read in time ~ units / w and joined in
   // ~ w / rows; the sum is least where w^2 ~ units * rows.
-  // Above one for each CU it is two for each: three for two CUs take as long as four.
+  // Above one for each CU it is the same number for each: three for two CUs take as long as four.
   int64_t fit = min(units / kMinUnits, (int64_t)(kSplit * __builtin_amdgcn_sqrtf((float)units * (float)(places * rows_of_place))));
-  if (fit > p.cus && fit < p.blocks) fit = p.cus;
+  if (fit > p.cus && fit < p.blocks) fit -= fit % p.cus;
   const int64_t active = fit < 1 ? 1 : (fit < p.blocks ? fit : p.blocks);
   if (units == 0 || (int64_t)blockIdx.x >= active) {
     if (threadIdx.x == 0) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -427,9 +439,10 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
 
       K keys;
       const uint8_t *b0 = half(ta, 0), *b1 = half(ta, 1);
-      keys.load(b0, b1);
+      if (ahead) keys.load(b0, b1);
       for (int32_t t = ta; t < tb; ++t) {
         const int left = len - t * kTile;  // tokens from here on
+        if (!ahead) keys.load(b0, b1);
         V vals;
         vals.load(b0 + to_v, b1 + to_v, 0);
         const uint8_t *v0 = b0 + to_v, *v1 = b1 + to_v;
@@ -441,7 +454,7 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
         if (t + 1 < tb) {
           b0 = half(t + 1, 0);
           b1 = half(t + 1, 1);
-          keys.load(b0, b1);
+          if (ahead) keys.load(b0, b1);
         }
         float zs[8];
 #pragma unroll
@@ -492,6 +505,7 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
     // To LDS: a lane has channels 128 c + CW (4 grp + x) + k of its head in o[c CW + k][x].
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (hd < heads) {
+      float *const mine_at = sum_at(wave, slot, hd);
 #pragma unroll
       for (int c = 0; c < NV; ++c)
 #pragma unroll
@@ -499,7 +513,7 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
 #pragma unroll
           for (int k = 0; k < CW; ++k) {
             const int ch = 128 * c + CW * (4 * grp + x) + k;
-            if (D >= 16 || ch < D) os[wave][slot][hd][ch] = o[c * CW + k][x];
+            if (D >= 16 || ch < D) mine_at[ch] = o[c * CW + k][x];
           }
       if (grp == 0) {
         sm[wave][slot][hd] = m;
@@ -513,7 +527,7 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
         const int hh = v / D, ch = v - hh * D;
         const int64_t q = row_at + my_tile * kHeads + hh;
         const float mx = sm[wave][1][hh], ls = sl[wave][1][hh], f = ls == 0.0f ? 0.0f : vs / ls;
-        const f32x4 x = *reinterpret_cast<const f32x4 *>(&os[wave][1][hh][ch]);
+        const f32x4 x = *reinterpret_cast<const f32x4 *>(sum_at(wave, 1, hh) + ch);
         *reinterpret_cast<uint2 *>(p.out + q * D + ch) = make_uint2(pack_bf16(x[0] * f, x[1] * f), pack_bf16(x[2] * f, x[3] * f));
         if (p.lse && ch == 0) p.lse[q] = ls == 0.0f ? -INFINITY : (mx + __builtin_log2f(ls)) * kLn2;
       }
@@ -553,7 +567,7 @@ __global__ __launch_bounds__(64 * waves_of(D), blocks_per_cu(D)) void k_attend(P
           const int w = ((k >> 1) << log2q) + tile;
           const float e = __builtin_amdgcn_exp2f(ms[k] - mb);
           ls = __builtin_fmaf(e, sl[w][k & 1][hw], ls);
-          const f32x4 x = *reinterpret_cast<const f32x4 *>(&os[w][k & 1][hw][ch]);
+          const f32x4 x = *reinterpret_cast<const f32x4 *>(sum_at(w, k & 1, hw) + ch);
 #pragma unroll
           for (int c = 0; c < 4; ++c) ov[c] = __builtin_fmaf(e, x[c], ov[c]);
         }
@@ -661,7 +675,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(PGeo g, AttendA
 }
 
 struct Plan {
-  int group, tiles_q, shared_q, kept, blocks, slot;
+  int group, tiles_q, shared_q, kept, cus, blocks, slot, lds;
   int64_t bytes;
 };
 
@@ -671,10 +685,20 @@ Plan attend_plan(const PGeo &g, int64_t q_heads) {
   p.tiles_q = (p.group + kHeads - 1) / kHeads;
   p.shared_q = p.tiles_q == 1 ? 1 : (p.tiles_q == 2 ? 2 : waves_of(g.D));
   p.kept = p.group < kHeads * p.shared_q ? p.group : kHeads * p.shared_q;
-  p.blocks = device_cu_count() * blocks_per_cu(g.D);
+  p.lds = waves_of(g.D) * 2 * (p.group < kHeads ? p.group : kHeads) * row_floats(g.D) * (int)sizeof(float);
+  const int by_lds = kLds / (p.lds + 2048), by_regs = waves_per_simd(g.fmt, g.D) * 4 / waves_of(g.D);
+  p.cus = device_cu_count();
+  p.blocks = p.cus * (by_lds < by_regs ? by_lds : by_regs);
   p.slot = p.kept * g.D + (2 * p.kept + 3) / 4 * 4;
   p.bytes = p.blocks * ((int64_t)sizeof(int4) + 2 * (int64_t)sizeof(float) * p.slot);
   return p;
+}
+
+template <int FMT, int D>
+void launch_attend(const PGeo &g, const skv_pages &pages, int layer, const AttendArgs &p, int lds, int32_t *status, hipStream_t st) {
+  const dim3 grid((uint32_t)p.blocks), block(64 * waves_of(D));
+  if (p.tiles_q == 1) k_attend<FMT, D, 1><<<grid, block, lds, st>>>(g, pages, layer, p, status);
+  else k_attend<FMT, D, 0><<<grid, block, lds, st>>>(g, pages, layer, p, status);
 }
 
 }  // namespace
@@ -727,12 +751,11 @@ extern "C" int skv_attend(const skv_pages_shape *shape, const skv_pages *pages, 
   // no more workgroups than the longest sequences that the table holds could use
   const __int128 units = (__int128)n * g.heads * plan.tiles_q * (((int64_t)g.max_tokens + kTile - 1) / kTile) / kMinUnits + 1;
   p.blocks = units < plan.blocks ? (int)units : plan.blocks;
-  p.cus = plan.blocks / blocks_per_cu(g.D);
+  p.cus = plan.cus;
   p.split = static_cast<int4 *>(workspace);
   p.part = reinterpret_cast<float *>(p.split + p.blocks);
-  const dim3 grid((uint32_t)p.blocks);
   hipStream_t st = static_cast<hipStream_t>(stream);
-#define SKV_ATTEND(F_, D_) case D_: k_attend<F_, D_><<<grid, 64 * waves_of(D_), 0, st>>>(g, *pages, (int)layer, p, status); break
+#define SKV_ATTEND(F_, D_) case D_: launch_attend<F_, D_>(g, *pages, (int)layer, p, plan.lds, status, st); break
 #define SKV_ATTEND_ALL(F_) \
   switch (g.D) { \
     SKV_ATTEND(F_, 8); SKV_ATTEND(F_, 16); SKV_ATTEND(F_, 32); SKV_ATTEND(F_, 64); \
