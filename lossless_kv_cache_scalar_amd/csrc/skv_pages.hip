@@ -108,6 +108,38 @@ __device__ __forceinline__ bool failed(const int *err, int32_t *hdr, int32_t *st
   return true;
 }
 
+// holders of pages p .. p + 3 (p a multiple of 4); behind the last page 1, neither free nor counted on
+__device__ __forceinline__ int4 refs_of(const PGeo &g, const skv_pages &a, int64_t p) {
+  if (p + 4 <= g.n_pages) return *reinterpret_cast<const int4 *>(a.refs + p);
+  int4 r = make_int4(1, 1, 1, 1);
+  if (p < g.n_pages) r.x = a.refs[p];
+  if (p + 1 < g.n_pages) r.y = a.refs[p + 1];
+  if (p + 2 < g.n_pages) r.z = a.refs[p + 2];
+  return r;
+}
+
+// ---- rows and pages named in a list of at most kPlan places: hash tables in LDS ----
+constexpr int kSlots = 2 * kPlan;
+
+__device__ __forceinline__ int slot_of(int32_t key) { return (int)(((uint32_t)key * 2654435761u) >> 21) & (kSlots - 1); }
+// the slot of a key that is put in; `had`: it was there
+__device__ __forceinline__ int put_key(int *keys, int32_t key, bool &had) {
+  for (int i = slot_of(key);; i = (i + 1) & (kSlots - 1)) {  // at most half of the slots are ever taken
+    const int old = atomicCAS(&keys[i], -1, key);
+    had = old == key;
+    if (old == -1 || had) return i;
+  }
+}
+__device__ __forceinline__ bool has_key(const int *keys, int32_t key) {
+  for (int i = slot_of(key);; i = (i + 1) & (kSlots - 1)) {
+    const int k = keys[i];
+    if (k == key || k == -1) return k == key;
+  }
+}
+__device__ __forceinline__ void clear_keys(int *keys) {
+  for (int i = threadIdx.x; i < kSlots; i += kPlan) keys[i] = -1;
+}
+
 // ---- extend ----
 // Which listed sequences copy their last page: with c sharers in the list and r
 // holders in all, every one of them where r > c, all but the last where r = c.
@@ -184,14 +216,7 @@ __global__ __launch_bounds__(kPlan) void k_plan_extend_long(PGeo g, skv_pages a,
   int64_t found = 0;
   for (int64_t base = 0; base < g.n_pages && found < need_all; base += (int64_t)kPlan * 4) {
     const int64_t p = base + (int64_t)tid * 4;
-    int4 r = make_int4(1, 1, 1, 1);
-    if (p + 4 <= g.n_pages) {
-      r = *reinterpret_cast<const int4 *>(a.refs + p);
-    } else {
-      if (p < g.n_pages) r.x = a.refs[p];
-      if (p + 1 < g.n_pages) r.y = a.refs[p + 1];
-      if (p + 2 < g.n_pages) r.z = a.refs[p + 2];
-    }
+    const int4 r = refs_of(g, a, p);
     const int f0 = r.x == 0, f1 = r.y == 0, f2 = r.z == 0, f3 = r.w == 0;
     int64_t t;
     int64_t at = found + block_scan(f0 + f1 + f2 + f3, t, lds);
@@ -241,18 +266,7 @@ __global__ __launch_bounds__(kPlan) void k_plan_extend_long(PGeo g, skv_pages a,
 // The same for lists of at most kPlan places, a thread to each: what the list
 // says stays in registers, and rows and pages are found again in hash tables in
 // LDS instead of through memory (64 rows: 6 us against 11).
-constexpr int kSlots = 2 * kPlan;
 constexpr int kFree = 2048;  // free pages that LDS holds; more go through the workspace
-
-__device__ __forceinline__ int slot_of(int32_t key) { return (int)(((uint32_t)key * 2654435761u) >> 21) & (kSlots - 1); }
-// the slot of a key that is put in; `had`: it was there
-__device__ __forceinline__ int put_key(int *keys, int32_t key, bool &had) {
-  for (int i = slot_of(key);; i = (i + 1) & (kSlots - 1)) {  // at most half of the slots are ever taken
-    const int old = atomicCAS(&keys[i], -1, key);
-    had = old == key;
-    if (old == -1 || had) return i;
-  }
-}
 
 __global__ __launch_bounds__(kPlan) void k_plan_extend(PGeo g, skv_pages a, const int32_t *__restrict__ seqs,
                                                        const int32_t *__restrict__ n_new, int n, PWork w,
@@ -265,13 +279,12 @@ __global__ __launch_bounds__(kPlan) void k_plan_extend(PGeo g, skv_pages a, cons
   __shared__ int32_t fl[kFree];
   const int tid = threadIdx.x;
   const int32_t s = tid < n ? seqs[tid] : -1, add = tid < n ? n_new[tid] : 0;
+  int4 held4 = refs_of(g, a, (int64_t)tid * 4);  // the first ones, long before they are looked at
   if (tid == 0) err = 0;
-  for (int i = tid; i < kSlots; i += kPlan) {
-    row_key[i] = -1;
-    page_key[i] = -1;
-    page_cnt[i] = 0;
-    page_last[i] = -1;
-  }
+  clear_keys(row_key);
+  clear_keys(page_key);
+  clear_keys(page_last);
+  for (int i = tid; i < kSlots; i += kPlan) page_cnt[i] = 0;
   __syncthreads();
   int32_t len = 0, page = -1, held = 0;
   if (s >= 0) {
@@ -323,14 +336,7 @@ __global__ __launch_bounds__(kPlan) void k_plan_extend(PGeo g, skv_pages a, cons
   int64_t found = 0;
   for (int64_t base = 0; base < g.n_pages && found < need_all; base += (int64_t)kPlan * 4) {
     const int64_t p = base + (int64_t)tid * 4;
-    int4 r = make_int4(1, 1, 1, 1);
-    if (p + 4 <= g.n_pages) {
-      r = *reinterpret_cast<const int4 *>(a.refs + p);
-    } else {
-      if (p < g.n_pages) r.x = a.refs[p];
-      if (p + 1 < g.n_pages) r.y = a.refs[p + 1];
-      if (p + 2 < g.n_pages) r.z = a.refs[p + 2];
-    }
+    const int4 r = base == 0 ? held4 : refs_of(g, a, p);
     int64_t t;
     int64_t k = found + block_scan((r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0), t, lds);
     const int32_t rs[4] = {r.x, r.y, r.z, r.w};
@@ -444,26 +450,37 @@ __global__ __launch_bounds__(kPlan) void k_check_fork(PGeo g, skv_pages a, const
                                                       const int32_t *__restrict__ dst,
                                                       const int32_t *__restrict__ n_tokens, int n, int apply, PWork w,
                                                       int32_t *status) {
-  __shared__ int err;
+  __shared__ int err, keys[kSlots];
   if (threadIdx.x == 0) err = 0;
+  clear_keys(keys);
   __syncthreads();
+  const bool few = n <= kPlan;
   for (int i = threadIdx.x; i < n; i += kPlan) {
-    const int32_t s = src[i], d = dst[i];
+    const int32_t s = src[i], d = dst[i], to = n_tokens ? n_tokens[i] : 0;
     if (s < 0 || d < 0) continue;
     if (s >= g.max_seqs || d >= g.max_seqs) { note(&err, SKV_ERR_ARG); continue; }
     const int32_t len = a.lens[s];
-    if (len < 0 || len > g.max_tokens || a.lens[d] != 0) note(&err, SKV_ERR_ARG);
-    if (n_tokens && (n_tokens[i] < 0 || n_tokens[i] > len)) note(&err, SKV_ERR_ARG);
-    agent_store(&w.mark[s], -1);
-    agent_store(&w.mark[d], -1);
+    if (len < 0 || len > g.max_tokens || a.lens[d] != 0 || to < 0 || to > len) note(&err, SKV_ERR_ARG);
+    if (few) {
+      bool had;
+      put_key(keys, d, had);
+      if (had) note(&err, SKV_ERR_ARG);
+    } else {
+      agent_store(&w.mark[s], -1);
+      agent_store(&w.mark[d], -1);
+    }
   }
-  if (failed(&err, w.hdr, status)) return;
-  for (int i = threadIdx.x; i < n; i += kPlan)
-    if (src[i] >= 0 && dst[i] >= 0) agent_store(&w.mark[dst[i]], i);
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kPlan)
-    if (src[i] >= 0 && dst[i] >= 0 && (agent_load(&w.mark[dst[i]]) != i || agent_load(&w.mark[src[i]]) != -1))
-      note(&err, SKV_ERR_ARG);
+  if (!few) {
+    for (int i = threadIdx.x; i < n; i += kPlan)
+      if (src[i] >= 0 && dst[i] >= 0 && src[i] < g.max_seqs && dst[i] < g.max_seqs) agent_store(&w.mark[dst[i]], i);
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < n; i += kPlan) {
+    const int32_t s = src[i], d = dst[i];
+    if (s < 0 || d < 0 || s >= g.max_seqs || d >= g.max_seqs) continue;
+    if (few ? has_key(keys, s) : agent_load(&w.mark[d]) != i || agent_load(&w.mark[s]) != -1) note(&err, SKV_ERR_ARG);
+  }
   if (failed(&err, w.hdr, status)) return;
   if (threadIdx.x == 0) w.hdr[kHdrOk] = 1;
   if (!apply) return;
@@ -483,20 +500,30 @@ __global__ __launch_bounds__(256) void k_fork(PGeo g, skv_pages a, const int32_t
 __global__ __launch_bounds__(kPlan) void k_check_truncate(PGeo g, skv_pages a, const int32_t *__restrict__ seqs,
                                                           const int32_t *__restrict__ keep, int n, int apply, PWork w,
                                                           int32_t *status) {
-  __shared__ int err;
+  __shared__ int err, keys[kSlots];
   if (threadIdx.x == 0) err = 0;
+  clear_keys(keys);
   __syncthreads();
+  const bool few = n <= kPlan;
   for (int i = threadIdx.x; i < n; i += kPlan) {
-    const int32_t s = seqs[i];
+    const int32_t s = seqs[i], to = keep ? keep[i] : 0;
     if (s < 0) continue;
     if (s >= g.max_seqs) { note(&err, SKV_ERR_ARG); continue; }
-    const int32_t len = a.lens[s], to = keep ? keep[i] : 0;
+    const int32_t len = a.lens[s];
     if (len < 0 || len > g.max_tokens || to < 0 || to > len) note(&err, SKV_ERR_ARG);
-    agent_store(&w.mark[s], i);
+    if (few) {
+      bool had;
+      put_key(keys, s, had);
+      if (had) note(&err, SKV_ERR_ARG);
+    } else {
+      agent_store(&w.mark[s], i);
+    }
   }
-  if (failed(&err, w.hdr, status)) return;
-  for (int i = threadIdx.x; i < n; i += kPlan)
-    if (seqs[i] >= 0 && agent_load(&w.mark[seqs[i]]) != i) note(&err, SKV_ERR_ARG);
+  if (!few) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kPlan)
+      if (seqs[i] >= 0 && seqs[i] < g.max_seqs && agent_load(&w.mark[seqs[i]]) != i) note(&err, SKV_ERR_ARG);
+  }
   if (failed(&err, w.hdr, status)) return;
   if (threadIdx.x == 0) w.hdr[kHdrOk] = 1;
   if (!apply) return;
@@ -514,25 +541,36 @@ __global__ __launch_bounds__(256) void k_truncate(PGeo g, skv_pages a, const int
 }
 
 // ---- compact ----
+// four pages to a thread; free and used pages are counted in the two halves of one sum
 __global__ __launch_bounds__(kPlan) void k_plan_compact(PGeo g, skv_pages a, int32_t *n_live, PWork w) {
   __shared__ int64_t lds[kPlanWaves];
   const int tid = threadIdx.x;
+  const int64_t step = (int64_t)kPlan * 4;
+  const int4 first = refs_of(g, a, (int64_t)tid * 4);
+  auto used_of = [&](int64_t p, const int4 &r) {  // a bit per page
+    const int in = (int)max((int64_t)0, min((int64_t)4, g.n_pages - p));
+    return ((r.x > 0) | (r.y > 0) << 1 | (r.z > 0) << 2 | (r.w > 0) << 3) & ((1 << in) - 1);
+  };
   int64_t mine = 0, live;
-  for (int64_t p = tid; p < g.n_pages; p += kPlan) mine += a.refs[p] > 0;
+  for (int64_t p = (int64_t)tid * 4; p < g.n_pages; p += step) mine += __builtin_popcount(used_of(p, p < step ? first : refs_of(g, a, p)));
   block_scan(mine, live, lds);
   int64_t holes = 0, movers = 0;
-  for (int64_t base = 0; base < g.n_pages; base += kPlan) {
-    const int64_t p = base + tid;
-    const bool used = p < g.n_pages && a.refs[p] > 0;
-    const bool hole = p < live && !used, mover = p >= live && used;
-    int64_t t0, t1;
-    const int64_t h = block_scan(hole, t0, lds);
-    const int64_t m = block_scan(mover, t1, lds);
-    if (hole) agent_store(&w.cdst[holes + h], (int32_t)p);
-    if (mover) agent_store(&w.csrc[movers + m], (int32_t)p);
-    if (p >= live && p < g.n_pages) w.cnt[p] = -1;  // its new place, once it has one
-    holes += t0;
-    movers += t1;
+  for (int64_t base = 0; base < g.n_pages; base += step) {
+    const int64_t p = base + (int64_t)tid * 4;
+    const int used = used_of(p, base == 0 ? first : refs_of(g, a, p));
+    const int in = (int)max((int64_t)0, min((int64_t)4, g.n_pages - p)), low = (int)max((int64_t)0, min((int64_t)4, live - p));
+    const int hole = ~used & ((1 << low) - 1), mover = used & ~((1 << low) - 1);
+    int64_t all;
+    const int64_t before = block_scan((int64_t)__builtin_popcount(hole) << 32 | __builtin_popcount(mover), all, lds);
+    int64_t h = holes + (before >> 32), m = movers + (int32_t)before;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (hole >> c & 1) agent_store(&w.cdst[h++], (int32_t)p + c);
+      if (mover >> c & 1) agent_store(&w.csrc[m++], (int32_t)p + c);
+      if (c >= low && c < in) w.cnt[p + c] = -1;  // its new place, once it has one
+    }
+    holes += all >> 32;
+    movers += (int32_t)all;
   }
   __syncthreads();
   // as many free pages below n_live as used ones above it
