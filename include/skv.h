@@ -404,7 +404,7 @@ int skv_attend_workspace_size(const skv_pages_shape *shape, int64_t q_heads, siz
  *   q       (device) bf16 [n][q_heads][head_dim], rows q_stride elements apart
  *           (a multiple of 8, >= q_heads * head_dim); 16-byte aligned
  *   k_scale, v_scale  (device) fp32 [kv_heads], e4m3 caches only, or NULL (1)
- *   seqs    (device) int32 [n], rows may repeat
+ *   seqs    (device) int32 [n], n <= 65536; rows may repeat
  *   out     (device) bf16 [n][q_heads][head_dim], 16-byte aligned
  *   lse     (device) fp32 [n][q_heads], or NULL
  * Scores, softmax statistics and sums are fp32.  The result is the same for

@@ -33,6 +33,7 @@ constexpr float kSplit = 3.0f;
 // (registers: 256 or 512 to a wave)
 __host__ __device__ constexpr int waves_of(int D) { return D <= 256 ? 4 : 2; }
 __host__ __device__ constexpr int waves_per_simd(int fmt, int D) { return D <= 128 || (D == 256 && fmt == SKV_SYM_E4M3) ? 2 : 1; }
+constexpr int kMaxRows = 1 << 16;  // list places of a call
 constexpr int kLds = 160 * 1024;  // of a CU
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -74,18 +75,15 @@ struct Row {
 };
 
 // ---- the dealing out ----
-// the sequence of list place i (-1: padding, or none that the cache has) and its length
+// the sequence of a list place (-1: padding, or none that the cache has) and its length
 struct Place {
   int32_t s, len;
 };
-__device__ __forceinline__ Place place_of(const PGeo &g, const skv_pages &a, const AttendArgs &p, int i, bool &bad) {
+__device__ __forceinline__ int32_t listed(const AttendArgs &p, int i) { return i < p.n ? p.seqs[i] : -1; }
+__device__ __forceinline__ Place place_of(const PGeo &g, const skv_pages &a, int32_t s, bool &bad) {
   Place x = {-1, 0};
-  bad = false;
-  if (i >= p.n) return x;
-  const int32_t s = p.seqs[i];
-  if (s < 0) return x;
   bad = s >= g.max_seqs;
-  if (bad) return x;
+  if (s < 0 || bad) return x;
   x.s = s;
   x.len = a.lens[s];
   bad = x.len < 0 || x.len > g.max_tokens;
@@ -333,27 +331,54 @@ __global__ __launch_bounds__(64 * waves_of(D), waves_per_simd(FMT, D)) void k_at
   __shared__ Row rows[NW][2];                // by part of the run
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = lane & 15, grp = lane >> 4;
 
-  // units in all, and the place that this workgroup's run begins in
+  // Units of 32 tokens in each 64 places of the list, by the waves in turn, four
+  // times 64 places at once; and in all.
   const int rows_of_head = (p.tiles_q + p.shared_q - 1) / p.shared_q, rows_of_place = g.heads * rows_of_head;
-  int64_t before = 0;  // units of 32 tokens in the places before the 64 at hand
-  int64_t places = 0;
-  int chunk = 0;       // the first of them
-  Place place;         // the lane's
-  uint32_t upto = 0;   // of those at hand, up to and with the lane's
+  const int chunks = (p.n + 63) / 64;
+  __shared__ uint32_t chunk_tiles[kMaxRows / 64];
+  __shared__ int32_t chunk_places[kMaxRows / 64];
   bool bad;
-  auto look = [&]() {
-    place = place_of(g, a, p, chunk + lane, bad);
-    upto = wave_scan(place.s >= 0 ? (uint32_t)tiles_of(place.len) : 0);  // 64 lengths of 2^30 at most: 2^31
-  };
-  for (;;) {
-    look();
+  Place place;         // the lane's of the 64 places at hand
+  uint32_t upto = 0;   // units of those, up to and with the lane's; 64 lengths of 2^30 at most: 2^31
+  int64_t all = 0, places = 0;
+  if (chunks == 1) {
+    place = place_of(g, a, listed(p, lane), bad);
+    upto = wave_scan(place.s >= 0 ? (uint32_t)tiles_of(place.len) : 0);
+    all = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+    places = __builtin_popcountll(__builtin_amdgcn_ballot_w64(place.s >= 0));
     if (bad && blockIdx.x == 0) set_status(status, SKV_ERR_ARG);
-    places += __builtin_popcountll(__builtin_amdgcn_ballot_w64(place.s >= 0));
-    if (chunk + 64 >= p.n) break;
-    before += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
-    chunk += 64;
+  } else {
+    constexpr int R = 4;
+    for (int c = wave; c < chunks; c += NW * R) {
+      int32_t s[R];
+      Place x[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) s[r] = listed(p, (c + NW * r) * 64 + lane);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        x[r] = place_of(g, a, s[r], bad);
+        if (bad && blockIdx.x == 0) set_status(status, SKV_ERR_ARG);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint32_t t = wave_scan(x[r].s >= 0 ? (uint32_t)tiles_of(x[r].len) : 0);
+        const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(x[r].s >= 0));
+        if (lane == 63 && c + NW * r < chunks) {
+          chunk_tiles[c + NW * r] = t;
+          chunk_places[c + NW * r] = n;
+        }
+      }
+    }
+    __syncthreads();
+    for (int c = 0; c < chunks; c += 64) {
+      // 64 sums of 2^31 at most: in two halves
+      const uint32_t t = c + lane < chunks ? chunk_tiles[c + lane] : 0;
+      all += (uint32_t)__builtin_amdgcn_readlane((int)wave_scan(t & 0xFFFF), 63);
+      all += (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)wave_scan(t >> 16), 63) << 16;
+      places += (uint32_t)__builtin_amdgcn_readlane((int)wave_scan(c + lane < chunks ? (uint32_t)chunk_places[c + lane] : 0), 63);
+    }
   }
-  const int64_t units = (before + (uint32_t)__builtin_amdgcn_readlane((int)upto, 63)) * rows_of_place;
+  const int64_t units = all * rows_of_place;
   // workgroups that take part: not so many that a row's join costs more than the
   // split saves.  With w of them a row is read in time ~ units / w and joined in
   // ~ w / rows; the sum is least where w^2 ~ units * rows.
@@ -373,23 +398,24 @@ __global__ __launch_bounds__(64 * waves_of(D), waves_per_simd(FMT, D)) void k_at
   int64_t u = run + ((run_end - run) * my_part >> log2p);
   const int64_t begun = u, end = run + ((run_end - run) * (my_part + 1) >> log2p);
   if (my_tile == 0 && lane < 2) rows[my_part][lane].tiles = 0;
-  if (chunk > 0) {
-    before = 0;
-    chunk = 0;
-    look();
-  }
+  int64_t before = 0;  // units of 32 tokens in the places before those at hand
+  int chunk = 0;       // the 64 at hand
+  bool looked = chunks == 1;
   while (u < end) {
     // the place of unit u: the first whose units reach beyond it
-    uint64_t beyond = __builtin_amdgcn_ballot_w64((before + upto) * rows_of_place > u);
-    while (beyond == 0 && chunk + 64 < p.n) {
-      before += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
-      chunk += 64;
-      look();
-      beyond = __builtin_amdgcn_ballot_w64((before + upto) * rows_of_place > u);
+    while (chunks > 1 && chunk + 1 < chunks && (before + chunk_tiles[chunk]) * rows_of_place <= u) {
+      before += chunk_tiles[chunk++];
+      looked = false;
     }
+    if (!looked) {
+      place = place_of(g, a, listed(p, chunk * 64 + lane), bad);
+      upto = wave_scan(place.s >= 0 ? (uint32_t)tiles_of(place.len) : 0);
+      looked = true;
+    }
+    const uint64_t beyond = __builtin_amdgcn_ballot_w64((before + upto) * rows_of_place > u);
     if (beyond == 0) break;  // only where lengths change under the call
     const int at = __builtin_ctzll(beyond);
-    const int i = chunk + at;
+    const int i = chunk * 64 + at;
     const int32_t s = __builtin_amdgcn_readlane(place.s, at), len = __builtin_amdgcn_readlane(place.len, at);
     const int32_t tiles = tiles_of(len);
     const int64_t in_place = u - (before + (uint32_t)__builtin_amdgcn_readlane((int)upto, at) - tiles) * rows_of_place;
@@ -686,7 +712,7 @@ Plan attend_plan(const PGeo &g, int64_t q_heads) {
   p.shared_q = p.tiles_q == 1 ? 1 : (p.tiles_q == 2 ? 2 : waves_of(g.D));
   p.kept = p.group < kHeads * p.shared_q ? p.group : kHeads * p.shared_q;
   p.lds = waves_of(g.D) * 2 * (p.group < kHeads ? p.group : kHeads) * row_floats(g.D) * (int)sizeof(float);
-  const int by_lds = kLds / (p.lds + 2048), by_regs = waves_per_simd(g.fmt, g.D) * 4 / waves_of(g.D);
+  const int by_lds = kLds / (p.lds + 10 * 1024), by_regs = waves_per_simd(g.fmt, g.D) * 4 / waves_of(g.D);
   p.cus = device_cu_count();
   p.blocks = p.cus * (by_lds < by_regs ? by_lds : by_regs);
   p.slot = p.kept * g.D + (2 * p.kept + 3) / 4 * 4;
@@ -722,7 +748,7 @@ extern "C" int skv_attend(const skv_pages_shape *shape, const skv_pages *pages, 
   if ((e = check_pages(pages)) != SKV_OK) return e;
   size_t need = 0;
   if ((e = skv_attend_workspace_size(shape, q_heads, &need)) != SKV_OK) return e;
-  if (layer < 0 || layer >= g.layers || n < 0 || n > (1 << 20) || !status || !aligned4(status)) return SKV_ERR_ARG;
+  if (layer < 0 || layer >= g.layers || n < 0 || n > kMaxRows || !status || !aligned4(status)) return SKV_ERR_ARG;
   if (!workspace || !aligned16(workspace) || workspace_bytes < need) return SKV_ERR_ARG;
   if (!isfinite(scale)) return SKV_ERR_ARG;
   if (n == 0) return SKV_OK;

@@ -129,7 +129,7 @@ def test_long_ragged_batch(fmt):
     c.compare(0, q, list(range(8)), out, lse)
 
 
-@pytest.mark.parametrize("rows", [257, 1000])
+@pytest.mark.parametrize("rows", [64, 65, 128, 257, 1000, 6000])
 def test_many_rows(rows):
     """More rows than a workgroup has threads, padded and empty ones among them."""
     lens = [(7 * i) % 50 for i in range(120)]
@@ -138,6 +138,16 @@ def test_many_rows(rows):
     q = c.q(rows)
     out, lse = c.attend(0, q, seqs)
     c.compare(0, q, seqs, out, lse)
+
+
+def test_rows_beyond_the_first_four_thousand():
+    """Long rows at both ends of a list whose places between are padded, empty or short."""
+    c = Case(1, [3000, 5, 0, 2500], 64, 64, 2, 4, layers=1)
+    seqs = [0] + [(-1, 2, 1)[i % 3] for i in range(4300)] + [3, 0]
+    q = c.q(len(seqs))
+    out, lse = c.attend(0, q, seqs)
+    pick = [0, 1, 2, 3, 64, 66, 4298, 4299, 4300, 4301, 4302]
+    c.compare(0, q[pick], [seqs[i] for i in pick], out[pick], lse[pick])
 
 
 @pytest.mark.parametrize("fmt,D,kv_heads,group", [(0, 128, 8, 2), (1, 64, 4, 20), (0, 512, 2, 33)])

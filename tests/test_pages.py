@@ -99,7 +99,7 @@ def test_attend_checks_its_arguments(lib):
     args = [S, good, 1, P, 384, 6, 0.125, None, None, P, 3, P, None, P, ws, P, None]
     _refused(lib.skv_attend, args, holed + [
         (0, None), (1, None), (2, -1), (2, 2), (3, None), (3, P + 8), (4, 376), (4, 388), (4, 1 << 62), (5, 0), (5, -2), (5, 5),
-        (6, float("nan")), (6, float("inf")), (7, P), (8, P), (9, None), (10, -1), (11, None), (11, P + 2), (12, P + 2), (13, None),
+        (6, float("nan")), (6, float("inf")), (7, P), (8, P), (9, None), (10, -1), (10, 65537), (11, None), (11, P + 2), (12, P + 2), (13, None),
         (13, P + 8), (14, ws - 1), (15, None)])
     args[10] = 0
     assert lib.skv_attend(*args) == skv.OK
