@@ -41,10 +41,17 @@ def parse():
     return p.parse_args()
 
 
+# sources that hold none of the coder's kernels: host entry points, the paged cache and its attention
+NOT_CODER = ("skv_api.hip", "skv_attend.hip", "skv_pages.hip", "skv_pages.hpp")
+
+
 def csrc_hash() -> str:
+    """Hash of the coder's kernel sources, which the counter records were taken on."""
     h = hashlib.sha256()
     d = os.path.join(ROOT, "lossless_kv_cache_scalar_amd", "csrc")
     for f in sorted(os.listdir(d)):
+        if f in NOT_CODER:
+            continue
         with open(os.path.join(d, f), "rb") as fh:
             h.update(f.encode() + fh.read())
     return h.hexdigest()[:16]
