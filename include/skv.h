@@ -405,7 +405,7 @@ int skv_attend_workspace_size(const skv_pages_shape *shape, int64_t q_heads, siz
  *           (a multiple of 8, >= q_heads * head_dim); 16-byte aligned
  *   k_scale, v_scale  (device) fp32 [kv_heads], e4m3 caches only, or NULL (1)
  *   seqs    (device) int32 [n], n <= 65536; rows may repeat
- *   out     (device) bf16 [n][q_heads][head_dim], 16-byte aligned
+ *   out     (device) bf16 [n][q_heads][head_dim], 16-byte aligned, apart from q
  *   lse     (device) fp32 [n][q_heads], or NULL
  * Scores, softmax statistics and sums are fp32.  The result is the same for
  * every call with the same inputs on the same GPU model.  SKV_ERR_ARG (status):

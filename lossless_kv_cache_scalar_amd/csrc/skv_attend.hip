@@ -17,6 +17,16 @@
 // tokens, columns: heads), so that a lane holds eight tokens' scores of one
 // head; the same lane's weights are then the operand of O^T += V^T P^T as they
 // lie, and no value crosses lanes but the maximum.
+//
+// What bounds it.  Every cached symbol is read once and used for 2 to 32
+// operations a byte, far below what the matrix units need to be the limit: it is
+// HBM.  64 sequences of up to 8192 tokens (64 query and 8 KV heads of 128, bf16,
+// 1.08 GB): 169 us and 5 for the join, 6.2 TB/s, of the 7.0 that a plain read
+// reaches here; inside the loop it is 6.85, the rest is the start (three dependent
+// loads before the first key, 2.3 us), the last waves' tail (the older workgroup
+// of a CU ends first) and the join.  16 sequences up to 32768 in e4m3 (0.81 GB):
+// 127 + 5 us.  One sequence of 2048 tokens (8.4 MB) takes 7.0 + 2.7 us, which is
+// latency: a chain of six loads, two launches.
 #include <math.h>
 
 #include "skv_pages.hpp"
@@ -27,7 +37,13 @@ namespace {
 
 constexpr int kTile = 32;    // tokens of a unit
 constexpr int kHeads = 16;   // query heads of a tile
-constexpr int kMinUnits = 4; // units of a workgroup at least
+// Units of a workgroup at least: one to a wave (8 KV heads of 128, one sequence
+// of 2048 tokens in bf16: 10.3 us; with 8 or 16 it is 11.8 and 13.5, with 2 the
+// same and the short calls 9.7 against 10.4).
+constexpr int kMinUnits = 4;
+// Workgroups are limited to kSplit sqrt(units * rows), see below.  At 1.5 that
+// sequence takes 12.2 us instead of 9.9, one of 2^20 tokens over one KV head 146
+// instead of 110; without a limit one of 65536 takes 37 instead of 32.
 constexpr float kSplit = 3.0f;
 // waves of a workgroup (LDS holds two partial sums of each), and of a SIMD
 // (registers: 256 or 512 to a wave)

@@ -358,7 +358,8 @@ class Pages:
     with (0: no attend).  Every call enqueues on `stream` or the current one and
     returns at once; errors that the device finds stay in `status` until
     `check()` reads and clears them.  Lists are int32 tensors on the cache's
-    device, which has to be the current one.
+    device, which has to be the current one.  The object's calls share its
+    workspaces: on several streams they have to be ordered.
     """
 
     def __init__(self, sh: SkvPagesShape, pool=None, table=None, lens=None, refs=None, q_heads: int = 0, device="cuda"):
@@ -376,9 +377,13 @@ class Pages:
             refs = torch.empty(sh.n_pages, dtype=torch.int32, device=device)
         self.shape, self.q_heads, self._head_dim = sh, int(q_heads), sh.head_dim
         self.pool, self.table, self.lens, self.refs = pool, table, lens, refs
-        _fits(pool, pool_bytes, "pool")
-        for t, n, what in ((table, sh.max_seqs * sh.max_pages, "table"), (lens, sh.max_seqs, "lens"), (refs, sh.n_pages, "refs")):
-            _int32(t, n, what)
+        # a larger array has other rows than the library takes it to have
+        esz = 2 if sh.sym_fmt == SYM_BF16 else 1
+        if pool.element_size() != esz or pool.numel() * esz != pool_bytes or not pool.is_contiguous():
+            raise SkvError(f"pool: contiguous, {pool_bytes // esz} elements of {esz} bytes wanted")
+        for t, want, what in ((table, (sh.max_seqs, sh.max_pages), "table"), (lens, (sh.max_seqs,), "lens"), (refs, (sh.n_pages,), "refs")):
+            if t.dtype is not torch.int32 or t.shape != want or not t.is_contiguous():
+                raise SkvError(f"{what}: contiguous int32 {list(want)} wanted")
         self.device, self._index = pool.device, pool.get_device() if pool.is_cuda else None
         for t, what in ((pool, "pool"), (table, "table"), (lens, "lens"), (refs, "refs")):
             self._here(t, what)
@@ -438,9 +443,8 @@ class Pages:
     def _scales(self, t, what: str):
         if t is None:
             return None
-        if t.dtype != torch.float32:
-            raise SkvError(f"{what}: {t.dtype}, float32 wanted")
-        _fits(t, 4 * self.shape.kv_heads, what)
+        if t.dtype is not torch.float32 or t.shape != (self.shape.kv_heads,) or not t.is_contiguous():
+            raise SkvError(f"{what}: {t.dtype} {list(t.shape)}, contiguous float32 {[self.shape.kv_heads]} wanted")
         self._here(t, what)
         return t.data_ptr()
 
@@ -555,8 +559,3 @@ class Pages:
                                  self._st, self._call(stream)), "skv_attend")
         return out
 
-
-def _int32(t, n: int, what: str):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
-        raise SkvError(f"{what}: an int32 tensor is wanted")
-    _fits(t, 4 * n, what)

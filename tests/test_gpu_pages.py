@@ -463,3 +463,73 @@ def test_calls_on_another_stream():
         assert torch.equal(out.view(torch.int16), pages.attend(0, q, seqs).view(torch.int16))
         pages.truncate(seqs, stream=s)
     st.synchronize()
+
+
+def test_two_caches_on_two_streams_at_once():
+    """Two caches' steps enqueued in turn on two streams, nothing between them waiting: each as alone."""
+    g = torch.Generator().manual_seed(9)
+    kv = [torch.randn(600, 2, 2, 128, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2)]
+    q = [torch.randn(3, 8, 128, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2)]
+    rows, more, forked = ints([0, 1]), ints([590, 5]), ints([2])
+    seqs, pos = ints([0] * 590 + [1] * 5), ints(list(range(590)) + list(range(5)))
+    one, zero, asked = ints([1]), ints([0]), ints([2, 0, 1])
+
+    def step(pages, i, stream):
+        pages.extend(rows, more, stream=stream)
+        pages.store(0, kv[i][:595, 0], kv[i][:595, 1], seqs, pos, stream=stream)
+        pages.fork(zero, forked, stream=stream)
+        pages.extend(forked, one, stream=stream)
+        pages.store(0, kv[i][595:596, 0], kv[i][595:596, 1], forked, ints590, stream=stream)
+        return pages.attend(0, q[i], asked, stream=stream)
+
+    ints590 = ints([590])
+    sh = skv.pages_shape(1, 2, 128, 16, 90, 4, 40)
+    alone = [step(skv.Pages(sh, q_heads=8), i, None) for i in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        both_ = [skv.Pages(sh, q_heads=8) for _ in range(2)]
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        torch.cuda.synchronize()
+        outs = [step(both_[i], i, streams[i]) for i in range(2)]
+        torch.cuda.synchronize()
+        for i in range(2):
+            both_[i].check()
+            assert torch.equal(outs[i], alone[i])
+
+
+def test_captured_page_calls_replay():
+    """Fork, growth, compaction and freeing in one graph: each replay as the eager calls on a twin."""
+    sh = skv.pages_shape(2, 1, 64, 16, 30, 6, 6)
+    one, two = skv.Pages(sh), skv.Pages(sh)
+    x = torch.randint(0, 1000, (2, 2, 1, 60, 64), dtype=torch.int16, device=DEV)
+    for p in (one, two):
+        p.extend(ints([5]), ints([40]))  # pages that the compaction has to pass over later
+        p.extend(ints([0, 1]), ints([21, 60]))
+        p.scatter(0, 0, 21, x[:, :, :, :21].contiguous())
+        p.scatter(1, 0, 60, x)
+        p.truncate(ints([5]))
+    src, dst, part, grow, keep = ints([0, 1, 0]), ints([2, 3, 4]), ints([21, 50, 5]), ints([1, 1, 20]), ints([0, 1, 0])
+    live = [torch.zeros(1, dtype=torch.int32, device=DEV) for _ in range(2)]
+
+    def step(p, n):
+        p.fork(src, dst, part)
+        p.extend(dst, grow)
+        p.truncate(dst, keep)
+        p.compact(n)
+        p.truncate(ints3)
+
+    ints3 = ints([3])
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step(one, live[0])
+    for k in range(4):
+        graph.replay()
+        step(two, live[1])
+        torch.cuda.synchronize()
+        assert live[0].item() == live[1].item() > 0
+        for a, b in ((one.table, two.table), (one.lens, two.lens), (one.refs, two.refs)):
+            assert torch.equal(a, b), k
+        assert torch.equal(one.gather(1, 0, 60), x) and torch.equal(two.gather(0, 0, 21), x[:, :, :, :21])
+    one.check()
+    two.check()

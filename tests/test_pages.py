@@ -119,5 +119,11 @@ def test_binding_refuses_other_types_and_devices(lib):
         skv.Pages(sh, pool, table.long(), lens, refs)
     with pytest.raises(skv.SkvError, match="contiguous"):
         skv.Pages(sh, pool, torch.zeros(8, 4, dtype=torch.int32).t(), lens, refs)
+    with pytest.raises(skv.SkvError, match="table"):
+        skv.Pages(sh, pool, torch.zeros(4, 16, dtype=torch.int32), lens, refs)  # rows of another length
+    with pytest.raises(skv.SkvError, match="refs"):
+        skv.Pages(sh, pool, table, lens, torch.zeros(9, dtype=torch.int32))
+    with pytest.raises(skv.SkvError, match="pool"):
+        skv.Pages(sh, pool.view(torch.uint8), table, lens, refs)
     with pytest.raises(skv.SkvError, match="pool: on cpu"):
         skv.Pages(sh, pool, table, lens, refs)
