@@ -11,7 +11,7 @@ struct PGeo {
   int64_t n_pages, max_seqs, max_pages;
   int64_t page_bytes;  // one page of one layer: 2 * heads * page_tokens * row_bytes, contiguous
   int layers, heads, D, P;
-  int log2P;
+  int log2P, log2D;
   int fmt;
   int esz;             // bytes of a symbol
   int row_bytes;       // one token of one (kv, head): D * esz
@@ -36,6 +36,7 @@ inline int make_pgeo(const skv_pages_shape *sh, PGeo &g) {
   g.D = (int)sh->head_dim;
   g.P = (int)sh->page_tokens;
   g.log2P = __builtin_ctz((unsigned)g.P);
+  g.log2D = __builtin_ctz((unsigned)g.D);
   g.n_pages = sh->n_pages;
   g.max_seqs = sh->max_seqs;
   g.max_pages = sh->max_pages;

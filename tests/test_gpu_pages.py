@@ -238,7 +238,7 @@ def test_store_every_bf16_value_as_e4m3():
     x = torch.arange(-32768, 32768, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(512, 1, 128)
     pages = skv.Pages(sh)
     pages.extend(ints([0]), ints([512]))
-    for scale in (1.0, 0.3, 7.0):
+    for scale in (1.0, 0.3, 7.0, -0.3, 448.0, 1.9999999, 2.0 ** -70, 2.0 ** -60, 2.0 ** 61, 0.0, float("inf"), float("nan")):
         sc = torch.full((1,), scale)
         xd = x.to(DEV)
         pages.store(0, xd, xd, ints([0] * 512), ints(range(512)), sc.to(DEV), None if scale == 1.0 else sc.to(DEV))
