@@ -14,8 +14,8 @@
 // Everything that moves symbols is bound by HBM and measured at its rate: moving
 // 250 of 500 pages of 64 layers (2.1 GB read and written) 410 us, 5.1 TB/s; the
 // coder's layout from or to 8192 tokens of 28 layers (0.94 GB) 157 us, 6.0 TB/s,
-// against 4.8 TB/s for a copy of 4 GiB; 16376 tokens stored as e4m3 (101 MB) 25 us,
-// 4.1 TB/s.
+// against 4.8 TB/s for a copy of 4 GiB; 16376 tokens stored as e4m3 (101 MB) 21 us,
+// 4.9 TB/s.
 #include "skv_pages.hpp"
 
 using namespace skv;
@@ -640,20 +640,19 @@ __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
 // division costs a dozen instructions.  With y = 1 / s rounded, q = a y and the
 // exact remainder r = q s - a (by fma), q - r y is that quotient for every bf16
 // mantissa a over every fp32 mantissa s (all 2^30 pairs were tried), so long as
-// nothing overflows, which the limits on s and |a| see to; a remainder that
-// underflows belongs to a quotient far below e4m3's smallest value.  With s > 0
-// zeros keep their signs.  16376 tokens of 2048 values: 31 us with divisions, 25 without.
+// nothing overflows, which the limits of 2^60 on s, 1 / s and |a| see to; a
+// remainder that underflows belongs to a quotient far below e4m3's smallest value.
+// With s > 0 zeros keep their signs.  Infinities, NaN and other scales take the
+// division.  16376 tokens of 2048 values: 31 us with divisions, 21 without.
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 struct Scale {
   float s, y;
-  uint32_t most;  // magnitudes (bf16 patterns) up to this take the short way; 0: none does
-  __device__ __forceinline__ explicit Scale(float scale) : s(scale), y(1.0f / scale) {
-    most = scale >= 0x1p-60f && scale <= 0x1p60f ? __float_as_uint(447.0f * scale) >> 16 : 0;
-  }
+  bool good;
+  __device__ __forceinline__ explicit Scale(float scale) : s(scale), y(1.0f / scale), good(scale >= 0x1p-60f && scale <= 0x1p60f) {}
   __device__ __forceinline__ float over(float a) const {
     const float q = a * y;
-    return __builtin_fmaf(-__builtin_fmaf(q, s, -a), y, q);
+    return __builtin_amdgcn_fmed3f(__builtin_fmaf(-__builtin_fmaf(q, s, -a), y, q), -448.0f, 448.0f);
   }
   __device__ __forceinline__ uint32_t four(uint32_t w0, uint32_t w1) const {
     const float a = __uint_as_float(w0 << 16), b = __uint_as_float(w0 & 0xFFFF0000u);
@@ -670,7 +669,7 @@ struct Scale {
       const uint32_t mag = x[c] & 0x7FFF7FFFu;
       m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, mag));
     }
-    if (__builtin_amdgcn_ballot_w64((uint32_t)max(m.x, m.y) > most || most == 0) == 0) return u32x2{four(x.x, x.y), four(x.z, x.w)};
+    if (__builtin_amdgcn_ballot_w64(!good || max(m.x, m.y) > 0x5D80) == 0) return u32x2{four(x.x, x.y), four(x.z, x.w)};
     return u32x2{two(x.x) | two(x.y) << 16, two(x.z) | two(x.w) << 16};
   }
 };
