@@ -12,7 +12,7 @@
 // loads and as many barriers: fork 2.6 us (2 rows) to 4.7 (32 rows of 64 pages),
 // extend 6.0 to 6.7, truncate 2.2 to 4.4, compaction's plan of 1000 pages 4.6.
 // Everything that moves symbols is bound by HBM and measured at its rate: moving
-// 250 of 500 pages of 64 layers (2.1 GB read and written) 410 us, 5.1 TB/s; the
+// 250 of 1000 pages of 64 layers (2.1 GB read and written) 410 us, 5.1 TB/s; the
 // coder's layout from or to 8192 tokens of 28 layers (0.94 GB) 157 us, 6.0 TB/s,
 // against 4.8 TB/s for a copy of 4 GiB; 16376 tokens stored as e4m3 (101 MB) 21 us,
 // 4.9 TB/s.
