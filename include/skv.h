@@ -407,7 +407,8 @@ int skv_attend_workspace_size(const skv_pages_shape *shape, int64_t q_heads, siz
  *   seqs    (device) int32 [n], n <= 65536; rows may repeat
  *   out     (device) bf16 [n][q_heads][head_dim], 16-byte aligned, apart from q
  *   lse     (device) fp32 [n][q_heads], or NULL
- * Scores, softmax statistics and sums are fp32.  The result is the same for
+ * Scores, softmax statistics and sums are fp32 (a sum of weights times values
+ * beyond its range is infinite).  The result is the same for
  * every call with the same inputs on the same GPU model.  SKV_ERR_ARG (status):
  * a row or page out of range, or a length beyond the table row; that row's
  * output is then unspecified.

@@ -220,6 +220,45 @@ def test_special_values():
     assert ((out[1] - ref[0]).abs() <= tol_out).all() and ((lse[1] - ref[1]).abs() <= tol_lse).all()
 
 
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_one_token_gives_its_value_back(fmt):
+    """With one token the weight is 1: every finite symbol comes out as the value it stands for, subnormal ones too."""
+    D = 512 if fmt == 0 else 256
+    c = Case(fmt, [1] * (65536 // D if fmt == 0 else 1), D, 16, 1, 1, layers=1)
+    n = len(c.lens)
+    pat = torch.arange(-32768, 32768, dtype=torch.int32).to(torch.int16) if fmt == 0 else torch.arange(256, dtype=torch.int32).to(torch.uint8)
+    pat = pat.view(n, D)
+    for s in range(n):
+        x = c.x[s].clone()
+        x[0, 1, 0, 0] = pat[s]
+        c.pages.scatter(s, 0, 1, x.to(DEV))
+    c.v_scale = c.k_scale = None
+    out = c.pages.attend(0, c.q(n).to(DEV), ints(range(n)))
+    c.pages.check()
+    want = values(pat.numpy(), fmt)
+    fine = torch.isfinite(want)
+    assert torch.equal(out.cpu().double().view(n, D)[fine], want[fine])
+
+
+def test_scores_of_subnormal_keys():
+    """A query picks one channel of keys that are subnormal e4m3 symbols: the scores are those values times the query's."""
+    c = Case(1, [256], 64, 16, 1, 1, layers=1)
+    x = c.x[0].clone()
+    x[0, 0] = 0
+    x[0, 0, 0, :, 5] = torch.arange(256, dtype=torch.int32).to(torch.uint8)  # one key for each symbol
+    x[0, 0, 0, [127, 255], 5] = 0
+    c.pages.scatter(0, 0, 256, x.to(DEV))
+    c.x[0] = x
+    c.k_scale = torch.ones(1)
+    c.v_scale = torch.ones(1)
+    for big in (1.0, 1024.0):
+        q = torch.zeros(1, 1, 64)
+        q[0, 0, 5] = big
+        q = q.to(torch.bfloat16)
+        out, lse = c.attend(0, q, [0], scale=1.0)
+        c.compare(0, q, [0], out, lse, 1.0)
+
+
 def test_broken_lists_are_reported_and_other_rows_right():
     c = Case(0, [40, 300, 20], 64, 16, 2, 4)
     q = c.q(3)
