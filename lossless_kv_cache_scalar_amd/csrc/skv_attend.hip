@@ -45,6 +45,7 @@ constexpr int kMinUnits = 4;
 // sequence takes 12.2 us instead of 9.9, one of 2^20 tokens over one KV head 146
 // instead of 110; without a limit one of 65536 takes 37 instead of 32.
 constexpr float kSplit = 3.0f;
+constexpr int kLongRow = 32;  // units of a row, on average, that make it a long one
 // waves of a workgroup (LDS holds two partial sums of each), and of a SIMD
 // (registers: 256 or 512 to a wave)
 __host__ __device__ constexpr int waves_of(int D) { return D <= 256 ? 4 : 2; }
@@ -398,8 +399,13 @@ __global__ __launch_bounds__(64 * waves_of(D), waves_per_simd(FMT, D)) void k_at
   // workgroups that take part: not so many that a row's join costs more than the
   // split saves.  With w of them a row is read in time ~ units / w and joined in
   // ~ w / rows; the sum is least where w^2 ~ units * rows.
-  // Above one for each CU it is the same number for each: three for two CUs take as long as four.
   int64_t fit = min(units / kMinUnits, (int64_t)(kSplit * __builtin_amdgcn_sqrtf((float)units * (float)(places * rows_of_place))));
+  // More than one for each CU pays where rows are short, so that workgroups wait
+  // for first loads often (64 sequences up to 512 tokens: 25.1 us with two, 28.4
+  // with one), or where there is much to read; 8 sequences of 2048 tokens take 22.2
+  // with two and 20.0 with one, 4 of 8192 30.5 and 28.3.
+  if (fit > p.cus && units >= kLongRow * places * rows_of_place) fit = max((int64_t)p.cus, min(fit, units / kLongRow));
+  // and it is the same number for each: three for two CUs take as long as four
   if (fit > p.cus && fit < p.blocks) fit -= fit % p.cus;
   const int64_t active = fit < 1 ? 1 : (fit < p.blocks ? fit : p.blocks);
   if (units == 0 || (int64_t)blockIdx.x >= active) {
