@@ -25,7 +25,7 @@
 // reaches here; inside the loop it is 6.85, the rest is the start (three dependent
 // loads before the first key, 2.3 us), the last waves' tail (the older workgroup
 // of a CU ends first) and the join.  16 sequences up to 32768 in e4m3 (0.81 GB):
-// 127 + 5 us.  One sequence of 2048 tokens (8.4 MB) takes 7.0 + 2.7 us, which is
+// 127 + 5 us.  One sequence of 2048 tokens (8.4 MB) takes 7.0 + 2.4 us, which is
 // latency: a chain of six loads, two launches.
 #include <math.h>
 
