@@ -39,12 +39,12 @@ enum { kHdrOk = 0, kHdrCopies = 1, kHdrLive = 2 };
 
 struct PWork {
   int32_t *hdr;    // 16 words
-  int32_t *mark;   // [max_seqs] last list place that names the row
-  int32_t *cnt;    // [n_pages] extend: listed sharers of a page; compact: where a page went
-  int32_t *owner;  // [n_pages] extend: the last of them; compact: free pages below n_live
-  int32_t *fl;     // [n_pages] free pages in order
-  int32_t *off;    // [max_seqs] extend: pages given out before a place's own
-  int32_t *cow;    // [max_seqs] extend: 1 where the last page is copied
+  int32_t *mark;   // [max_seqs] long lists: last list place that names the row
+  int32_t *cnt;    // [n_pages] extend, long lists: listed sharers of a page; compact: where a page went
+  int32_t *owner;  // [n_pages] extend, long lists: the last of them
+  int32_t *fl;     // [n_pages] extend: free pages in order
+  int32_t *off;    // [max_seqs] extend, long lists: pages given out before a place's own
+  int32_t *cow;    // [max_seqs] extend, long lists: 1 where the last page is copied
   int32_t *csrc;   // copies: source page, target page, tokens
   int32_t *cdst;
   int32_t *ctok;
