@@ -128,12 +128,6 @@ __device__ __forceinline__ int64_t lane_of(int64_t v, int l) {
   return (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
 }
 
-// a / b; of 32 bits where both are, as they are nearly always
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  if (((uint64_t)a | (uint64_t)b) >> 32) return a / b;
-  return (uint32_t)a / (uint32_t)b;
-}
-
 // Runs: of `units` units among `active` workgroups, the first `more` of which
 // have each + 1 and the others `each`.
 struct Runs {

@@ -744,7 +744,7 @@ constexpr int kMoveTokens = 64;
 
 template <typename U, int SCATTER>
 __global__ __launch_bounds__(256) void k_reorder(PGeo g, skv_pages a, int seq, int32_t first, int64_t tokens,
-                                                 int tiles, uint8_t *x, int32_t *status) {
+                                                 int tiles, int64_t item0, uint8_t *x, int32_t *status) {
   const int32_t len = a.lens[seq];
   if (len < 0 || len > g.max_tokens || first + tokens > len) {
     if (threadIdx.x == 0) set_status(status, SKV_ERR_ARG);
@@ -753,11 +753,10 @@ __global__ __launch_bounds__(256) void k_reorder(PGeo g, skv_pages a, int seq, i
   const uint32_t ru = (uint32_t)g.row_bytes / sizeof(U);  // a power of two
   const int lr = __builtin_ctz(ru);
   const int rows = 2 * g.heads;
-  const int64_t row = blockIdx.x / (uint32_t)tiles;
-  const int64_t l = row / rows;
+  const int64_t item = item0 + blockIdx.x, row = quotient(item, tiles), l = quotient(row, rows);
   const int kvh = (int)(row - l * rows);
   U *xr = reinterpret_cast<U *>(x) + (row * tokens << lr);
-  const int64_t t0 = (int64_t)(blockIdx.x - (uint32_t)row * tiles) * kMoveTokens;
+  const int64_t t0 = (item - row * tiles) * kMoveTokens;
   const uint32_t units = (uint32_t)min((int64_t)kMoveTokens, tokens - t0) << lr;
   for (uint32_t u = threadIdx.x; u < units; u += blockDim.x) {
     const int64_t t = t0 + (u >> lr);
@@ -931,16 +930,19 @@ extern "C" int skv_pages_store(const skv_pages_shape *shape, const skv_pages *pa
   const int64_t want = n * parts / (device_cu_count() * 4);
   const int64_t rounds = want / at_once < 1 ? 1 : (want / at_once < kStoreTokens ? want / at_once : kStoreTokens);
   const int64_t tokens = rounds * at_once < 256 ? rounds * at_once : 256;
-  const int64_t blocks = (n + tokens - 1) / tokens * parts;
-  if (blocks > INT32_MAX) return SKV_ERR_ARG;
+  const int64_t most = kMaxGrid / parts * tokens;  // of a launch
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const dim3 grid((uint32_t)blocks);
-  const uint16_t *kp = static_cast<const uint16_t *>(k), *vp = static_cast<const uint16_t *>(v);
-  if (g.fmt == SKV_SYM_E4M3)
-    k_store<1><<<grid, 256, 0, st>>>(g, *pages, (int)layer, kp, k_stride, vp, v_stride, k_scale, v_scale, seqs, pos, n, (int)tokens, (int)parts, status);
-  else
-    k_store<0><<<grid, 256, 0, st>>>(g, *pages, (int)layer, kp, k_stride, vp, v_stride, nullptr, nullptr, seqs, pos, n, (int)tokens, (int)parts, status);
-  return launched();
+  for (int64_t t = 0; t < n; t += most) {
+    const int64_t here = n - t < most ? n - t : most;
+    const dim3 grid((uint32_t)((here + tokens - 1) / tokens * parts));
+    const uint16_t *kp = static_cast<const uint16_t *>(k) + t * k_stride, *vp = static_cast<const uint16_t *>(v) + t * v_stride;
+    if (g.fmt == SKV_SYM_E4M3)
+      k_store<1><<<grid, 256, 0, st>>>(g, *pages, (int)layer, kp, k_stride, vp, v_stride, k_scale, v_scale, seqs + t, pos + t, here, (int)tokens, (int)parts, status);
+    else
+      k_store<0><<<grid, 256, 0, st>>>(g, *pages, (int)layer, kp, k_stride, vp, v_stride, nullptr, nullptr, seqs + t, pos + t, here, (int)tokens, (int)parts, status);
+    if ((e = launched()) != SKV_OK) return e;
+  }
+  return SKV_OK;
 }
 
 namespace {
@@ -954,22 +956,24 @@ int reorder(const skv_pages_shape *shape, const skv_pages *pages, int64_t seq, i
   if (first > g.max_tokens || tokens > g.max_tokens - first) return SKV_ERR_ARG;
   if (tokens == 0) return SKV_OK;
   if (!x || !aligned16(x)) return SKV_ERR_ARG;
-  const int64_t tiles64 = (tokens + kMoveTokens - 1) / kMoveTokens;
-  if ((__int128)g.layers * 2 * g.heads * tiles64 > INT32_MAX) return SKV_ERR_ARG;
-  const int tiles = (int)tiles64;
+  const int tiles = (int)((tokens + kMoveTokens - 1) / kMoveTokens);
+  const int64_t items = (int64_t)g.layers * 2 * g.heads * tiles;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const dim3 grid((uint32_t)((int64_t)g.layers * 2 * g.heads * tiles));
   uint8_t *xb = static_cast<uint8_t *>(x);
   const int32_t f = (int32_t)first;
   const int sq = (int)seq;
-  if (g.row_bytes >= 16) {
-    if (scatter) k_reorder<u32x4, 1><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, xb, status);
-    else k_reorder<u32x4, 0><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, xb, status);
-  } else {
-    if (scatter) k_reorder<u32x2, 1><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, xb, status);
-    else k_reorder<u32x2, 0><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, xb, status);
+  for (int64_t i = 0; i < items; i += kMaxGrid) {
+    const dim3 grid((uint32_t)(items - i < kMaxGrid ? items - i : kMaxGrid));
+    if (g.row_bytes >= 16) {
+      if (scatter) k_reorder<u32x4, 1><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, i, xb, status);
+      else k_reorder<u32x4, 0><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, i, xb, status);
+    } else {
+      if (scatter) k_reorder<u32x2, 1><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, i, xb, status);
+      else k_reorder<u32x2, 0><<<grid, 256, 0, st>>>(g, *pages, sq, f, tokens, tiles, i, xb, status);
+    }
+    if ((e = launched()) != SKV_OK) return e;
   }
-  return launched();
+  return SKV_OK;
 }
 }  // namespace
 

@@ -18,6 +18,11 @@ struct PGeo {
   int32_t max_tokens;  // max_pages * P
 };
 
+// Workgroups of a launch at most, where the number follows the data: HIP launches
+// fewer than 2^32 threads in all, which 2^24 workgroups of 256 would reach.  More
+// are launched in turn.
+constexpr int64_t kMaxGrid = 1 << 23;
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -63,6 +68,12 @@ __device__ __forceinline__ int32_t pages_of(int32_t tokens, const PGeo &g) {
 }
 
 __device__ __forceinline__ bool good_page(int32_t pg, const PGeo &g) { return (uint32_t)pg < (uint64_t)g.n_pages; }
+
+// a / b; of 32 bits where both are, as they are nearly always
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((uint64_t)a | (uint64_t)b) >> 32) return a / b;
+  return (uint32_t)a / (uint32_t)b;
+}
 
 // agent-scope accesses: read and written in L2, past the CU's own cache
 __device__ __forceinline__ int32_t agent_load(const int32_t *p) {
