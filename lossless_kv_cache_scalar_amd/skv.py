@@ -378,7 +378,8 @@ class Pages:
         self.shape, self.q_heads, self._head_dim = sh, int(q_heads), sh.head_dim
         self.pool, self.table, self.lens, self.refs = pool, table, lens, refs
         # a larger array has other rows than the library takes it to have
-        esz = 2 if sh.sym_fmt == SYM_BF16 else 1
+        self._esz = esz = 2 if sh.sym_fmt == SYM_BF16 else 1
+        self._token_symbols = sh.layers * 2 * sh.kv_heads * sh.head_dim
         if pool.element_size() != esz or pool.numel() * esz != pool_bytes or not pool.is_contiguous():
             raise SkvError(f"pool: contiguous, {pool_bytes // esz} elements of {esz} bytes wanted")
         for t, want, what in ((table, (sh.max_seqs, sh.max_pages), "table"), (lens, (sh.max_seqs,), "lens"), (refs, (sh.n_pages,), "refs")):
@@ -511,27 +512,51 @@ class Pages:
         return shape(self.shape.layers, self.shape.kv_heads, tokens, self.shape.head_dim, self.shape.sym_fmt, mu_fmt,
                      sigma_mode, phat_mode)
 
-    def _tokens(self, tokens, x):
-        sh = self.shape
-        _fits(x, sh.layers * 2 * sh.kv_heads * max(int(tokens), 0) * sh.head_dim * (2 if sh.sym_fmt == SYM_BF16 else 1), "x")
+    def _tokens(self, tokens: int, x) -> bool:
+        """Checks x, an array of `tokens` tokens in the coder's layout; True where its rows hold more tokens than
+        those, [layers][2][kv_heads][more][head_dim], so that the tokens to move lie apart in it."""
+        esz, n = self._esz, self._token_symbols * max(tokens, 0)
+        _fits(x, n * esz, "x")
         self._here(x, "x")
+        size, flat = x.element_size(), x.dim() == 1  # flat: packed at its start, whatever lies behind; bytes too
+        if size != esz and not (flat and x.dtype is torch.uint8):
+            raise SkvError(f"x: elements of {size} bytes, the symbols have {esz}")
+        if flat or x.numel() == n:
+            return False
+        rows, d = (self.shape.layers, 2, self.shape.kv_heads), self._head_dim
+        if x.dim() == 5 and x.shape[:3] == rows and x.shape[4] == d:
+            return True
+        raise SkvError(f"x: {list(x.shape)}, {[*rows, tokens, d]} wanted")
 
     def gather(self, seq: int, first: int, tokens: int, x=None, stream=None):
-        """skv_pages_gather: tokens [first, first + tokens) of a sequence in the coder's layout, as encode() takes them."""
-        sh = self.shape
+        """skv_pages_gather: tokens [first, first + tokens) of a sequence in the coder's layout, as encode() takes them.
+
+        x, where it is given, is [layers][2][kv_heads][tokens][head_dim] symbols, or a flat buffer that begins with
+        them.  Where its rows hold more tokens the first ones are written (through a copy); the coder wants them
+        packed."""
+        sh, tokens = self.shape, int(tokens)
         if x is None:
             with self._made_on(stream):
-                x = torch.empty(sh.layers, 2, sh.kv_heads, int(tokens), sh.head_dim, device=self.device,
+                x = torch.empty(sh.layers, 2, sh.kv_heads, tokens, sh.head_dim, device=self.device,
                                 dtype=torch.int16 if sh.sym_fmt == SYM_BF16 else torch.uint8)
-        self._tokens(tokens, x)
-        _check(self._lib.skv_pages_gather(self._sh, self._pg, int(seq), int(first), int(tokens), x.data_ptr(),
+        elif self._tokens(tokens, x):
+            part = x[:, :, :, :tokens]
+            with self._made_on(stream):
+                packed = part.contiguous()  # its symbols stay where the call writes none
+                self.gather(seq, first, tokens, packed, stream)
+                part.copy_(packed)
+            return x
+        _check(self._lib.skv_pages_gather(self._sh, self._pg, int(seq), int(first), tokens, x.data_ptr(),
                                        self._st, self._call(stream)), "skv_pages_gather")
         return x
 
     def scatter(self, seq: int, first: int, tokens: int, x, stream=None) -> None:
-        """skv_pages_scatter: the way back, from decode()'s output into the sequence's pages."""
-        self._tokens(tokens, x)
-        _check(self._lib.skv_pages_scatter(self._sh, self._pg, int(seq), int(first), int(tokens), x.data_ptr(),
+        """skv_pages_scatter: the way back, from decode()'s output into the sequence's pages; x as gather() takes it."""
+        tokens = int(tokens)
+        if self._tokens(tokens, x):
+            with self._made_on(stream):  # kept for the call by the order of its stream
+                x = x[:, :, :, :tokens].contiguous()
+        _check(self._lib.skv_pages_scatter(self._sh, self._pg, int(seq), int(first), tokens, x.data_ptr(),
                                         self._st, self._call(stream)), "skv_pages_scatter")
 
     def attend(self, layer: int, q, seqs, scale=None, k_scale=None, v_scale=None, out=None, lse=None, stream=None):

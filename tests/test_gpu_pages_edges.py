@@ -66,3 +66,68 @@ def test_store_of_more_work_than_a_launch_takes():
     want[[3 * j for j in range(len(at))]] = some
     for which in (0, 1):
         assert torch.equal(pages.pool[0, 0, which].transpose(0, 1), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_arrays_whose_rows_hold_more_tokens(fmt):
+    """gather and scatter between pages and the first tokens of each row of a longer array, on a stream of their own and in a graph too."""
+    sh = skv.pages_shape(2, 3, 64, 16, 20, 2, 8, fmt)
+    dt = torch.int16 if fmt == 0 else torch.uint8
+    g = torch.Generator().manual_seed(4)
+    want = torch.randint(0, 255, (2, 2, 3, 40, 64), generator=g).to(dt).to(DEV)
+    pages = skv.Pages(sh)
+    pages.extend(ints([0, 1]), ints([50, 50]))
+    long = torch.full((2, 2, 3, 99, 64), 7, dtype=dt, device=DEV)
+    long[:, :, :, :40] = want
+    pages.scatter(0, 9, 40, long)
+    assert torch.equal(pages.gather(0, 9, 40), want)
+    for stream in (None, torch.cuda.Stream()):
+        into = torch.full((2, 2, 3, 41, 64), 7, dtype=dt, device=DEV)
+        torch.cuda.synchronize()
+        assert pages.gather(0, 9, 40, into, stream=stream) is into
+        pages.scatter(1, 9, 40, into, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(into[:, :, :, :40], want) and (into[:, :, :, 40:] == 7).all()
+        assert torch.equal(pages.gather(1, 9, 40), want)
+        pages.scatter(1, 9, 40, torch.zeros_like(want))
+    into.fill_(7)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pages.gather(0, 9, 40, into)
+        pages.scatter(1, 9, 40, into)
+    for _ in range(3):
+        into.fill_(7)
+        graph.replay()
+        assert torch.equal(into[:, :, :, :40], want) and (into[:, :, :, 40:] == 7).all()
+        assert torch.equal(pages.gather(1, 9, 40), want)
+        pages.scatter(1, 9, 40, torch.zeros_like(want))
+    pages.check()
+    pages.gather(0, 11, 40, into)  # the sequence ends before: nothing is written
+    with pytest.raises(skv.SkvError, match="invalid argument"):
+        pages.check()
+    assert torch.equal(into[:, :, :, :40], want) and (into[:, :, :, 40:] == 7).all()
+
+
+def test_arrays_of_other_shapes_are_refused():
+    """A flat buffer begins with the packed symbols; any other array has exactly their number, and their size."""
+    sh = skv.pages_shape(2, 3, 64, 16, 20, 2, 8)
+    pages = skv.Pages(sh)
+    pages.extend(ints([0]), ints([50]))
+    n = 2 * 2 * 3 * 40 * 64
+    want = torch.randint(0, 1000, (2, 2, 3, 40, 64), dtype=torch.int16, device=DEV)
+    for x in (want, want.view(torch.bfloat16), want.view(12, -1), want.flatten(), want.flatten().view(torch.uint8),
+              torch.cat([want.flatten(), want.flatten()[:99]])):
+        pages.scatter(0, 3, 40, torch.zeros_like(want))
+        pages.scatter(0, 3, 40, x)
+        assert torch.equal(pages.gather(0, 3, 40), want)
+        back = torch.zeros_like(x)
+        assert pages.gather(0, 3, 40, back) is back
+        assert torch.equal(back.flatten().view(torch.int16)[:n], want.flatten())
+    for x in (torch.zeros(2, 2, 3, 41 * 64, dtype=torch.int16, device=DEV), torch.zeros(2, 2, 4, 40, 64, dtype=torch.int16, device=DEV),
+              torch.zeros(3, 2, 3, 40, 64, dtype=torch.int16, device=DEV), torch.zeros(2, 2, 3, 40, 65, dtype=torch.int16, device=DEV),
+              want.float(), want.view(torch.uint8), torch.zeros(2 * n, device=DEV), want[:, :, :, :39].contiguous(), want[:, :, :, :39]):
+        for call in (pages.gather, pages.scatter):
+            with pytest.raises(skv.SkvError, match="x: "):
+                call(0, 3, 40, x)
+    pages.check()
