@@ -41,12 +41,12 @@ def parse():
     return p.parse_args()
 
 
-# sources that hold none of the coder's kernels: host entry points, the paged cache and its attention
-NOT_CODER = ("skv_api.hip", "skv_attend.hip", "skv_pages.hip", "skv_pages.hpp")
+# sources that neither hold the coder's kernels nor set how they are launched
+NOT_CODER = ("skv_attend.hip", "skv_pages.hip", "skv_pages.hpp", "skv_status.hip")
 
 
 def csrc_hash() -> str:
-    """Hash of the coder's kernel sources, which the counter records were taken on."""
+    """Hash of the coder's sources, which the counter records were taken on: kernels, grids and workspace layout."""
     h = hashlib.sha256()
     d = os.path.join(ROOT, "lossless_kv_cache_scalar_amd", "csrc")
     for f in sorted(os.listdir(d)):
