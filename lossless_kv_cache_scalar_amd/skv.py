@@ -415,7 +415,10 @@ class Pages:
         """What a call makes itself is made on the call's stream."""
         if stream is None:
             return contextlib.nullcontext()
-        return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+        if not hasattr(stream, "cuda_stream"):  # an address; 0 is the default stream, which ExternalStream does not take
+            address = int(stream)
+            stream = torch.cuda.ExternalStream(address, self.device) if address else torch.cuda.default_stream(self.device)
+        return torch.cuda.stream(stream)
 
     def _list(self, t, n, what: str):
         if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32:

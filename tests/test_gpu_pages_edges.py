@@ -131,3 +131,29 @@ def test_arrays_of_other_shapes_are_refused():
             with pytest.raises(skv.SkvError, match="x: "):
                 call(0, 3, 40, x)
     pages.check()
+
+
+def test_address_0_is_the_default_stream():
+    """What a call makes, and what check() waits for, is the default stream's: work enqueued there before comes first."""
+    pages = skv.Pages(skv.pages_shape(1, 2, 64, 16, 20, 4, 8), q_heads=2)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with pages._made_on(0):
+            assert torch.cuda.current_stream() == torch.cuda.default_stream()
+        with pages._made_on(torch.cuda.default_stream()):
+            assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    busy = torch.randn(4096, 4096, device=DEV)
+    one, bad = ints([1]), ints([4])
+    q = torch.randn(1, 2, 64, device=DEV).to(torch.bfloat16)
+    pages.extend(one, ints([40]))
+    pages.scatter(1, 0, 40, torch.randint(0, 1000, (1, 2, 2, 40, 64), dtype=torch.int16, device=DEV))
+    want = pages.attend(0, q, one)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        busy = busy @ busy * 1e-3
+    out = pages.attend(0, q, one, stream=0)
+    live = pages.compact(stream=0)
+    pages.extend(bad, one, stream=0)
+    with pytest.raises(skv.SkvError, match="invalid argument"):
+        pages.check(stream=0)
+    pages.check(stream=0)
+    assert torch.equal(out, want) and int(live.item()) == 3
