@@ -397,7 +397,7 @@ class Pages:
         self._ws, self._aws, self._st = (t.data_ptr() for t in (self.workspace, self.attend_workspace, self.status))
         if new:
             self.reset()
-        torch.cuda.current_stream().synchronize()  # the arrays are ready for calls on any stream
+        torch.cuda.current_stream(self.device).synchronize()  # the arrays are ready for calls on any stream
 
     def _here(self, t, what: str):
         if t.get_device() != self._index:  # -1: on the host

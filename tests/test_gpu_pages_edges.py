@@ -157,3 +157,13 @@ def test_address_0_is_the_default_stream():
         pages.check(stream=0)
     pages.check(stream=0)
     assert torch.equal(out, want) and int(live.item()) == 3
+
+
+def test_the_constructor_waits_on_the_device_of_its_arrays(monkeypatch):
+    """Not on the current one, which may be another as long as no call is made."""
+    asked, real = [], torch.cuda.current_stream
+    sh = skv.pages_shape(1, 2, 64, 16, 20, 4, 8)
+    made = skv.Pages(sh)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: (asked.append(device), real(device))[1])
+    skv.Pages(sh, made.pool, made.table, made.lens, made.refs)
+    assert asked == [made.pool.device]
