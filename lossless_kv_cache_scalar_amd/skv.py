@@ -359,7 +359,10 @@ class Pages:
     returns at once; errors that the device finds stay in `status` until
     `check()` reads and clears them.  Lists are int32 tensors on the cache's
     device, which has to be the current one.  The object's calls share its
-    workspaces: on several streams they have to be ordered.
+    workspaces: on several streams they have to be ordered.  Tensors may be
+    dropped after a call on the current stream, as after torch's own operations, or
+    on a torch.cuda.Stream; those of a call on an address or an ExternalStream are
+    to be kept until it has run, as in C.
     """
 
     def __init__(self, sh: SkvPagesShape, pool=None, table=None, lens=None, refs=None, q_heads: int = 0, device="cuda"):
@@ -376,6 +379,7 @@ class Pages:
             lens = torch.empty(sh.max_seqs, dtype=torch.int32, device=device)
             refs = torch.empty(sh.n_pages, dtype=torch.int32, device=device)
         self.shape, self.q_heads, self._head_dim = sh, int(q_heads), sh.head_dim
+        self._streams = set()  # on which the arrays were used by name
         self.pool, self.table, self.lens, self.refs = pool, table, lens, refs
         # a larger array has other rows than the library takes it to have
         self._esz = esz = 2 if sh.sym_fmt == SYM_BF16 else 1
@@ -403,13 +407,25 @@ class Pages:
         if t.get_device() != self._index:  # -1: on the host
             raise SkvError(f"{what}: on {t.device}, not on the cache's GPU")
 
-    def _call(self, stream):
-        """The stream of a call, once the cache's device is seen to be the current one."""
+    def _call(self, stream, *given):
+        """The stream of a call on the tensors `given`, once the cache's device is seen to be the current one."""
         if torch.cuda.current_device() != self._index:
             raise SkvError(f"the cache is on {self.device}, the current device is cuda:{torch.cuda.current_device()}")
         if stream is None and _raw_stream is not None:  # a tenth of the time of the Stream object
             return _raw_stream(self._index)
+        self._keep(stream, *given)
         return _stream(stream)
+
+    def _keep(self, stream, *given):
+        """The tensors' memory, and the cache's own, goes to no other tensor before the stream has done with it.  An
+        external stream may be gone by the time that a tensor is freed, and is not named to the allocator."""
+        if isinstance(stream, torch.cuda.Stream) and not isinstance(stream, torch.cuda.ExternalStream):
+            if stream.cuda_stream not in self._streams:
+                self._streams.add(stream.cuda_stream)
+                given += (self.pool, self.table, self.lens, self.refs, self.workspace, self.attend_workspace, self.status)
+            for t in given:
+                if t is not None:
+                    t.record_stream(stream)
 
     def _made_on(self, stream):
         """What a call makes itself is made on the call's stream."""
@@ -470,7 +486,7 @@ class Pages:
         n = self._list(seqs, None, "seqs")
         self._list(n_new, n, "n_new")
         _check(self._lib.skv_pages_extend(self._sh, self._pg, seqs.data_ptr(), n_new.data_ptr(), n, self._ws,
-                                       self.ws_bytes, self._st, self._call(stream)), "skv_pages_extend")
+                                       self.ws_bytes, self._st, self._call(stream, seqs, n_new)), "skv_pages_extend")
 
     def fork(self, src, dst, n_tokens=None, stream=None) -> None:
         """skv_pages_fork: row dst[i] shares the pages of row src[i] (of its first n_tokens[i] tokens)."""
@@ -480,7 +496,7 @@ class Pages:
             self._list(n_tokens, n, "n_tokens")
         _check(self._lib.skv_pages_fork(self._sh, self._pg, src.data_ptr(), dst.data_ptr(), _ptr(n_tokens), n,
                                      self._ws, self.ws_bytes, self._st,
-                                     self._call(stream)), "skv_pages_fork")
+                                     self._call(stream, src, dst, n_tokens)), "skv_pages_fork")
 
     def truncate(self, seqs, keep=None, stream=None) -> None:
         """skv_pages_truncate: keep keep[i] tokens of sequence seqs[i]; free the rows without keep."""
@@ -488,7 +504,7 @@ class Pages:
         if keep is not None:
             self._list(keep, n, "keep")
         _check(self._lib.skv_pages_truncate(self._sh, self._pg, seqs.data_ptr(), _ptr(keep), n, self._ws,
-                                         self.ws_bytes, self._st, self._call(stream)), "skv_pages_truncate")
+                                         self.ws_bytes, self._st, self._call(stream, seqs, keep)), "skv_pages_truncate")
 
     def compact(self, n_live=None, stream=None):
         """skv_pages_compact; the number of pages in use, an int32 tensor of one."""
@@ -497,7 +513,7 @@ class Pages:
                 n_live = torch.empty(1, dtype=torch.int32, device=self.device)
         self._list(n_live, 1, "n_live")
         _check(self._lib.skv_pages_compact(self._sh, self._pg, n_live.data_ptr(), self._ws, self.ws_bytes,
-                                        self._st, self._call(stream)), "skv_pages_compact")
+                                        self._st, self._call(stream, n_live)), "skv_pages_compact")
         return n_live
 
     def store(self, layer: int, k, v, seqs, pos, k_scale=None, v_scale=None, stream=None) -> None:
@@ -508,7 +524,7 @@ class Pages:
         vs = self._rows(v, n, self.shape.kv_heads, "v")
         _check(self._lib.skv_pages_store(self._sh, self._pg, int(layer), k.data_ptr(), ks, v.data_ptr(), vs,
                                       self._scales(k_scale, "k_scale"), self._scales(v_scale, "v_scale"), seqs.data_ptr(),
-                                      pos.data_ptr(), n, self._st, self._call(stream)), "skv_pages_store")
+                                      pos.data_ptr(), n, self._st, self._call(stream, k, v, seqs, pos, k_scale, v_scale)), "skv_pages_store")
 
     def coder_shape(self, tokens: int, mu_fmt=MU_BF16, sigma_mode=SIGMA_CHANNEL, phat_mode=PHAT_STATIC) -> SkvShape:
         """The coder's shape of `tokens` tokens of one sequence."""
@@ -544,23 +560,25 @@ class Pages:
                                 dtype=torch.int16 if sh.sym_fmt == SYM_BF16 else torch.uint8)
         elif self._tokens(tokens, x):
             part = x[:, :, :, :tokens]
+            self._keep(stream, x)
             with self._made_on(stream):
                 packed = part.contiguous()  # its symbols stay where the call writes none
                 self.gather(seq, first, tokens, packed, stream)
                 part.copy_(packed)
             return x
         _check(self._lib.skv_pages_gather(self._sh, self._pg, int(seq), int(first), tokens, x.data_ptr(),
-                                       self._st, self._call(stream)), "skv_pages_gather")
+                                       self._st, self._call(stream, x)), "skv_pages_gather")
         return x
 
     def scatter(self, seq: int, first: int, tokens: int, x, stream=None) -> None:
         """skv_pages_scatter: the way back, from decode()'s output into the sequence's pages; x as gather() takes it."""
         tokens = int(tokens)
         if self._tokens(tokens, x):
+            self._keep(stream, x)
             with self._made_on(stream):  # kept for the call by the order of its stream
                 x = x[:, :, :, :tokens].contiguous()
         _check(self._lib.skv_pages_scatter(self._sh, self._pg, int(seq), int(first), tokens, x.data_ptr(),
-                                        self._st, self._call(stream)), "skv_pages_scatter")
+                                        self._st, self._call(stream, x)), "skv_pages_scatter")
 
     def attend(self, layer: int, q, seqs, scale=None, k_scale=None, v_scale=None, out=None, lse=None, stream=None):
         """skv_attend: attention of q [n][q_heads][head_dim], one token of each sequence in seqs, over the cached
@@ -584,6 +602,6 @@ class Pages:
         _check(self._lib.skv_attend(self._sh, self._pg, int(layer), q.data_ptr(), qs, self.q_heads, float(scale),
                                  self._scales(k_scale, "k_scale"), self._scales(v_scale, "v_scale"), seqs.data_ptr(), n,
                                  out.data_ptr(), _ptr(lse), self._aws, self.attend_bytes,
-                                 self._st, self._call(stream)), "skv_attend")
+                                 self._st, self._call(stream, q, k_scale, v_scale, seqs, out, lse)), "skv_attend")
         return out
 

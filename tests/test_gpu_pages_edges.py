@@ -167,3 +167,90 @@ def test_the_constructor_waits_on_the_device_of_its_arrays(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: (asked.append(device), real(device))[1])
     skv.Pages(sh, made.pool, made.table, made.lens, made.refs)
     assert asked == [made.pool.device]
+
+
+def test_tensors_dropped_after_a_call_on_a_stream():
+    """Lists, queries and whole caches whose last name goes while the stream has yet to come to the call: their memory is not given out."""
+    st = torch.cuda.Stream()
+    sh = skv.pages_shape(1, 2, 64, 16, 20, 4, 8, skv.SYM_E4M3)
+    pages = skv.Pages(sh, q_heads=2)
+    with torch.cuda.stream(st):
+        busy = torch.randn(4096, 4096, device=DEV)
+    torch.cuda.synchronize()
+
+    def dropped(call, *tensors):
+        """The call, with the stream busy before it; the tensors' addresses."""
+        with torch.cuda.stream(st):
+            a = busy
+            for _ in range(20):
+                a = a @ busy
+        call(*tensors)
+        assert not st.query()
+        return [(t.data_ptr(), t.numel(), t.dtype) for t in tensors]
+
+    def later(places):
+        """New tensors of the same sizes lie elsewhere while the stream is at work."""
+        keep = [torch.empty(n, dtype=dt, device=DEV) for _, n, dt in places for _ in range(40)]
+        assert not st.query()
+        assert not {p for p, _, _ in places} & {t.data_ptr() for t in keep}
+        st.synchronize()
+
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    f32 = dict(dtype=torch.float32, device=DEV)
+    later(dropped(lambda a, b: pages.extend(a, b, stream=st), ints([1]), ints([40])))
+    later(dropped(lambda k, v, s, p, x, y: pages.store(0, k, v, s, p, x, y, stream=st), torch.ones(2, 2, 64, **bf), torch.ones(2, 2, 64, **bf),
+                  ints([1, 1]), ints([3, 4]), torch.ones(2, **f32), torch.ones(2, **f32)))
+    later(dropped(lambda a, b, c: pages.fork(a, b, c, stream=st), ints([1]), ints([2]), ints([33])))
+    for n in (40, 41):
+        later(dropped(lambda x: pages.gather(1, 0, 40, x, stream=st), torch.zeros(1, 2, 2, n, 64, dtype=torch.uint8, device=DEV)))
+    for n in (1, 7):
+        later(dropped(lambda x: pages.scatter(2, 32, 1, x, stream=st), torch.zeros(1, 2, 2, n, 64, dtype=torch.uint8, device=DEV)))
+    assert int(pages.status.item()) == skv.ERR_ARG  # token 32 lies in a page that row 1 holds too
+    pages.status.zero_()
+    later(dropped(lambda q, s, x, y, o, l: pages.attend(0, q, s, k_scale=x, v_scale=y, out=o, lse=l, stream=st), torch.ones(1, 2, 64, **bf), ints([1]),
+                  torch.ones(2, **f32), torch.ones(2, **f32), torch.zeros(1, 2, 64, **bf), torch.zeros(1, 2, **f32)))
+    later(dropped(lambda a, b: pages.truncate(a, b, stream=st), ints([2]), ints([1])))
+    later(dropped(lambda n: pages.compact(n, stream=st), ints([0])))
+    pages.check()
+    assert pages.lens.tolist() == [0, 40, 1, 0]
+    own = [pages.pool, pages.table, pages.lens, pages.refs, pages.workspace, pages.attend_workspace, pages.status]
+    row, one = ints([3]), ints([1])
+    places = dropped(lambda *own: pages.extend(row, one, stream=st), *own)
+    del own, pages
+    later(places)
+    # named by its address, as in C, the stream is not told to the allocator: the caller keeps the tensors
+    pages = skv.Pages(sh)
+    pages.extend(row, one, stream=st.cuda_stream)
+    torch.cuda.synchronize()
+    pages.check()
+
+
+def test_captured_calls_that_name_their_stream():
+    """The capturing stream given by name, arguments dropped within the capture; replays as the eager calls, and the cache dropped after."""
+    sh = skv.pages_shape(1, 2, 64, 16, 20, 4, 8)
+    x = torch.randint(0, 1000, (1, 2, 2, 40, 64), dtype=torch.int16, device=DEV)
+    q = torch.randn(2, 2, 64, device=DEV).to(torch.bfloat16)
+    one, two = skv.Pages(sh, q_heads=2), skv.Pages(sh, q_heads=2)
+    rows, grow, out = ints([1, 2]), ints([40, 3]), torch.zeros_like(q)
+
+    def step(p, stream):
+        p.extend(rows.clone(), grow.clone(), stream=stream)
+        p.scatter(1, 0, 40, x.clone(), stream=stream)
+        p.attend(0, q.clone(), rows.clone(), out=out, stream=stream)
+        p.truncate(rows.clone(), stream=stream)
+
+    step(two, None)
+    want = out.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(one, torch.cuda.current_stream())
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want[0]) and int(one.lens.sum()) == 0
+    one.check()
+    del graph, one
+    torch.cuda.synchronize()
+    assert int(torch.zeros(4, device=DEV).sum()) == 0
