@@ -331,7 +331,7 @@ int skv_pages_extend(const skv_pages_shape *shape, const skv_pages *pages, const
  * them where n_tokens is NULL), holding the same pages; nothing is copied
  * until one of the holders grows.  src may repeat; every dst is a free row
  * (length 0), listed once and no src of this call.  A pair is padding where
- * either is negative.
+ * either is negative.  n <= max_seqs.
  *   SKV_ERR_ARG, cache unchanged: a row that breaks these rules, or n_tokens
  *   outside [0, length].
  */
@@ -341,7 +341,8 @@ int skv_pages_fork(const skv_pages_shape *shape, const skv_pages *pages, const i
 
 /*
  * Keep the first keep[i] tokens of sequence seqs[i] (none where keep is NULL:
- * the row is freed).  Pages that no token is left in are given back.
+ * the row is freed), i < n <= max_seqs.  Pages that no token is left in are given
+ * back.
  *   SKV_ERR_ARG, cache unchanged: a row out of range or listed twice, or
  *   keep[i] outside [0, length].
  */
@@ -359,8 +360,8 @@ int skv_pages_compact(const skv_pages_shape *shape, const skv_pages *pages, int3
                       void *workspace, size_t workspace_bytes, int32_t *status, void *stream);
 
 /*
- * Write keys and values of n tokens into layer `layer`: token i to position
- * pos[i] of sequence seqs[i], 0 <= pos[i] < its length.
+ * Write keys and values of n < 2^31 tokens into layer `layer`: token i to
+ * position pos[i] of sequence seqs[i], 0 <= pos[i] < its length.
  *   k, v      (device) bf16 [n][kv_heads][head_dim], rows k_stride, v_stride
  *             elements apart (multiples of 8, >= kv_heads * head_dim); 16-byte
  *             aligned
@@ -398,20 +399,22 @@ int skv_attend_workspace_size(const skv_pages_shape *shape, int64_t q_heads, siz
  * kv_heads query heads to a KV head, for query head j and h = j / g:
  *   z_t = scale * k_scale[h] * (q_j . k_{h,t})
  *   lse = log(sum_t exp(z_t)),  out_j = v_scale[h] * sum_t exp(z_t - lse) v_{h,t}
- * A sequence without tokens has out 0 and lse -inf.  What the pages hold behind
- * the last token is never used, NaN or not; a padded row's out and lse are left
- * as they are.
+ * A sequence without tokens, or with every score -inf, has out 0 and lse -inf.
+ * What the pages hold behind the last token is never used, NaN or not; a padded
+ * row's out and lse are left as they are.
  *   q       (device) bf16 [n][q_heads][head_dim], rows q_stride elements apart
  *           (a multiple of 8, >= q_heads * head_dim); 16-byte aligned
  *   k_scale, v_scale  (device) fp32 [kv_heads], e4m3 caches only, or NULL (1)
- *   seqs    (device) int32 [n], n <= 65536; rows may repeat
+ *   seqs    (device) int32 [n], n <= 65536 and n * q_heads < 2^31; rows may repeat
  *   out     (device) bf16 [n][q_heads][head_dim], 16-byte aligned, apart from q
  *   lse     (device) fp32 [n][q_heads], or NULL
  * Scores, softmax statistics and sums are fp32 (a sum of weights times values
- * beyond its range is infinite).  The result is the same for
- * every call with the same inputs on the same GPU model.  SKV_ERR_ARG (status):
- * a row or page out of range, or a length beyond the table row; that row's
- * output is then unspecified.
+ * beyond its range is infinite; a score above it gives NaN, one below it no
+ * weight).  The weights that multiply the values are rounded to bf16, to nearest
+ * even, each off by 2^-8 of itself at most; their sum and lse are taken before.
+ * The result is the same for every call with the same inputs on the same GPU
+ * model.  SKV_ERR_ARG (status): a row or page out of range, or a length beyond the
+ * table row; that row's output is then unspecified.
  */
 int skv_attend(const skv_pages_shape *shape, const skv_pages *pages, int64_t layer, const void *q,
                int64_t q_stride, int64_t q_heads, float scale, const float *k_scale, const float *v_scale,

@@ -18,15 +18,22 @@
 // head; the same lane's weights are then the operand of O^T += V^T P^T as they
 // lie, and no value crosses lanes but the maximum.
 //
-// What bounds it.  Every cached symbol is read once and used for 2 to 32
-// operations a byte, far below what the matrix units need to be the limit: it is
-// HBM.  64 sequences of up to 8192 tokens (64 query and 8 KV heads of 128, bf16,
-// 1.08 GB): 169 us and 5 for the join, 6.2 TB/s, of the 7.0 that a plain read
-// reaches here; inside the loop it is 6.85, the rest is the start (three dependent
-// loads before the first key, 2.3 us), the last waves' tail (the older workgroup
-// of a CU ends first) and the join.  16 sequences up to 32768 in e4m3 (0.81 GB):
-// 127 + 5 us.  One sequence of 2048 tokens (8.4 MB) takes 7.0 + 2.4 us, which is
-// latency: a chain of six loads, two launches.
+// What bounds it.  Up to 16 query heads to a KV head every cached symbol is read
+// once and used for 1 to 32 operations a byte, far below what the matrix units need
+// to be the limit: it is HBM.  64 sequences of up to 8192 tokens (64 query and 8 KV
+// heads of 128, bf16, 1.08 GB): 168 us and 5 for the join, 6.2 TB/s, of the 7.0 that
+// a plain read reaches here; inside the loop it is 6.85, the rest is the start (three
+// dependent loads before the first key, 2.3 us), the last waves' tail (the older
+// workgroup of a CU ends first) and the join.  16 sequences up to 32768 in e4m3
+// (0.81 GB): 127 + 5 us.  One sequence of 2048 tokens (8.4 MB) takes 7.1 + 2.2 us,
+// which is latency: a chain of six loads, two launches.  With more query heads each
+// tile of 16 asks for the same keys and values, through the caches, and from 65 (33
+// at 512 channels) on another row reads them from HBM again: 64 sequences of up to
+// 8192 with 20 heads to each of 4 KV heads (0.54 GB) take 119 us, with 40 to each of
+// 2 (0.27 GB) 86.  At 256 and 512 channels the values come 128 channels at a time,
+// each asked for after the products of those before, and the loop waits for them:
+// 64 sequences of up to 4096 over 8 KV heads of 256 in e4m3 (0.54 GB) take 112 us,
+// of up to 2048 over 8 of 512 in bf16 (1.08 GB) 219.
 #include <math.h>
 
 #include "skv_pages.hpp"
@@ -37,13 +44,15 @@ namespace {
 
 constexpr int kTile = 32;    // tokens of a unit
 constexpr int kHeads = 16;   // query heads of a tile
-// Units of a workgroup at least: one to a wave (8 KV heads of 128, one sequence
-// of 2048 tokens in bf16: 10.3 us; with 8 or 16 it is 11.8 and 13.5, with 2 the
-// same and the short calls 9.7 against 10.4).
+// Units of a workgroup at least: one to a wave (captured in a graph, 8 KV heads of
+// 128, one sequence of 2048 tokens in bf16: 8.9 us; with 2, 8 and 16 it is 9.4, 10.0
+// and 12.0; 7 sequences of up to 301 over 2 KV heads of 64: 9.3, and 8.7, 11.1, 14.6).
 constexpr int kMinUnits = 4;
-// Workgroups are limited to kSplit sqrt(units * rows), see below.  At 1.5 that
-// sequence takes 12.2 us instead of 9.9, one of 2^20 tokens over one KV head 146
-// instead of 110; without a limit one of 65536 takes 37 instead of 32.
+// Workgroups are limited to kSplit sqrt(units * rows), see below.  At 1.5 the one
+// sequence takes 11.3 us.  No limit at all is about as good: one sequence over one
+// KV head takes 11.6 us instead of 12.6 at 8192 tokens, 17.2 instead of 16.2 at 32768,
+// 27.6 instead of 28.0 at 131072.  Only the longest single rows want fewer: 2^20
+// tokens of one KV head take 98 us at 1.5 and 108 at 3.
 constexpr float kSplit = 3.0f;
 constexpr int kLongRow = 32;  // units of a row, on average, that make it a long one
 // waves of a workgroup (LDS holds two partial sums of each), and of a SIMD
@@ -170,8 +179,11 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
 // ---- a unit's keys and values in registers ----
-// Where each is read once it goes past the caches: 7.0 TB/s against 6.1 for a
-// plain read of 1 GiB.  Several tiles of query heads read the same ones.
+// Where one tile of query heads reads each it goes past the caches: 7.0 TB/s against
+// 6.1 for a plain read of 1 GiB, 169 us against 194 for the 64 sequences above.
+// Several tiles read the same ones.  Sequences that share pages do too, but far
+// apart in time; the memory-side cache serves them (32 forks of 8192 tokens, 8 KV
+// heads of 128 in bf16: 122 us, 8.8 TB/s of what the rows read, 34 MB of it distinct).
 template <int ONCE, typename T>
 __device__ __forceinline__ T fetched(const uint8_t *p) {
   if (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const T *>(p));
@@ -333,7 +345,7 @@ __global__ __launch_bounds__(64 * waves_of(D), waves_per_simd(FMT, D)) void k_at
   constexpr int row = K::row;
   constexpr int NW = waves_of(D);
   constexpr int LD = row_floats(D);
-  constexpr bool ahead = D <= 256;           // the next unit's keys are loaded during this one's softmax
+  constexpr bool ahead = D <= 256;           // the next unit's keys are asked for before this one's softmax
   // [NW][2][tile_heads][LD]: a wave's partial sums
   extern __shared__ float os[];
   const int tile_heads = min(p.group, kHeads);
@@ -395,9 +407,9 @@ __global__ __launch_bounds__(64 * waves_of(D), waves_per_simd(FMT, D)) void k_at
   // ~ w / rows; the sum is least where w^2 ~ units * rows.
   int64_t fit = min(units / kMinUnits, (int64_t)(kSplit * __builtin_amdgcn_sqrtf((float)units * (float)(places * rows_of_place))));
   // More than one for each CU pays where rows are short, so that workgroups wait
-  // for first loads often (64 sequences up to 512 tokens: 25.1 us with two, 28.4
-  // with one), or where there is much to read; 8 sequences of 2048 tokens take 22.2
-  // with two and 20.0 with one, 4 of 8192 30.5 and 28.3.
+  // for first loads often (64 sequences up to 512 tokens: 23.1 us with two, 27.1
+  // with one), or where there is much to read (up to 8192: 169 and 178); 8 sequences
+  // of 2048 tokens take 20.5 with two and 18.9 with one, 4 of 8192 31.6 and 29.4.
   if (fit > p.cus && units >= kLongRow * places * rows_of_place) fit = max((int64_t)p.cus, min(fit, units / kLongRow));
   // and it is the same number for each: three for two CUs take as long as four
   if (fit > p.cus && fit < p.blocks) fit -= fit % p.cus;

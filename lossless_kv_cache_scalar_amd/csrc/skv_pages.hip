@@ -9,13 +9,14 @@
 // copied goes to a list that a second, wide launch works through.
 //
 // What bounds them.  The planning launches are chains of three or four dependent
-// loads and as many barriers: fork 2.6 us (2 rows) to 4.7 (32 rows of 64 pages),
-// extend 6.0 to 6.7, truncate 2.2 to 4.4, compaction's plan of 1000 pages 4.6.
-// Everything that moves symbols is bound by HBM and measured at its rate: moving
-// 250 of 1000 pages of 64 layers (2.1 GB read and written) 410 us, 5.1 TB/s; the
-// coder's layout from or to 8192 tokens of 28 layers (0.94 GB) 157 us, 6.0 TB/s,
-// against 4.8 TB/s for a copy of 4 GiB; 16376 tokens stored as e4m3 (101 MB) 21 us,
-// 4.9 TB/s.
+// loads and as many barriers: fork 3 us (4 rows) to 5 (32 rows of 64 pages), extend
+// 6.3 to 6.8, truncate 2.7 to 4.6, compaction's plan of 1000 pages 4.7.  What moves
+// many symbols is bound by HBM: moving 250 of 1000 pages of 64 layers (2.07 GB read
+// and written) 359 to 420 us from box to box, 5.8 to 4.9 TB/s; the coder's layout
+// from 8192 tokens of 28 layers (0.94 GB) 150 us and back 163, 6.3 and 5.8 TB/s;
+// 16376 tokens stored as e4m3 (101 MB) 21 us, 4.8 TB/s.  A copy of 4 GiB reaches 4.8
+// to 4.9 TB/s here, a plain read 7.0.  The same tokens stored as bf16 (134 MB) take
+// 43 us, 3.1 TB/s: that kernel's registers leave a SIMD two waves (the e4m3 one eight).
 #include "skv_pages.hpp"
 
 using namespace skv;
