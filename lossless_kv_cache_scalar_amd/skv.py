@@ -531,9 +531,11 @@ class Pages:
         return shape(self.shape.layers, self.shape.kv_heads, tokens, self.shape.head_dim, self.shape.sym_fmt, mu_fmt,
                      sigma_mode, phat_mode)
 
-    def _tokens(self, tokens: int, x) -> bool:
-        """Checks x, an array of `tokens` tokens in the coder's layout; True where its rows hold more tokens than
-        those, [layers][2][kv_heads][more][head_dim], so that the tokens to move lie apart in it."""
+    def _tokens(self, tokens: int, x, stream) -> bool:
+        """Checks x, an array of `tokens` tokens in the coder's layout; False where the call is not made.
+
+        An array whose rows hold more tokens may be meant with those apart, or packed at its start as the coder would
+        read it: it is refused in the status, as a sequence that holds fewer tokens is."""
         esz, n = self._esz, self._token_symbols * max(tokens, 0)
         _fits(x, n * esz, "x")
         self._here(x, "x")
@@ -541,30 +543,26 @@ class Pages:
         if size != esz and not (flat and x.dtype is torch.uint8):
             raise SkvError(f"x: elements of {size} bytes, the symbols have {esz}")
         if flat or x.numel() == n:
-            return False
-        rows, d = (self.shape.layers, 2, self.shape.kv_heads), self._head_dim
-        if x.dim() == 5 and x.shape[:3] == rows and x.shape[4] == d:
             return True
-        raise SkvError(f"x: {list(x.shape)}, {[*rows, tokens, d]} wanted")
+        rows, d = (self.shape.layers, 2, self.shape.kv_heads), self._head_dim
+        if x.dim() != 5 or x.shape[:3] != rows or x.shape[4] != d:
+            raise SkvError(f"x: {list(x.shape)}, {[*rows, tokens, d]} wanted")
+        self._call(stream)
+        with self._made_on(stream):
+            self.status.masked_fill_(self.status == OK, ERR_ARG)
+        return False
 
     def gather(self, seq: int, first: int, tokens: int, x=None, stream=None):
         """skv_pages_gather: tokens [first, first + tokens) of a sequence in the coder's layout, as encode() takes them.
 
         x, where it is given, is [layers][2][kv_heads][tokens][head_dim] symbols, or a flat buffer that begins with
-        them.  Where its rows hold more tokens the first ones are written (through a copy); the coder wants them
-        packed."""
+        them.  One whose rows hold more tokens is left as it is, and check() reports an invalid argument."""
         sh, tokens = self.shape, int(tokens)
         if x is None:
             with self._made_on(stream):
                 x = torch.empty(sh.layers, 2, sh.kv_heads, tokens, sh.head_dim, device=self.device,
                                 dtype=torch.int16 if sh.sym_fmt == SYM_BF16 else torch.uint8)
-        elif self._tokens(tokens, x):
-            part = x[:, :, :, :tokens]
-            self._keep(stream, x)
-            with self._made_on(stream):
-                packed = part.contiguous()  # its symbols stay where the call writes none
-                self.gather(seq, first, tokens, packed, stream)
-                part.copy_(packed)
+        elif not self._tokens(tokens, x, stream):
             return x
         _check(self._lib.skv_pages_gather(self._sh, self._pg, int(seq), int(first), tokens, x.data_ptr(),
                                        self._st, self._call(stream, x)), "skv_pages_gather")
@@ -573,12 +571,9 @@ class Pages:
     def scatter(self, seq: int, first: int, tokens: int, x, stream=None) -> None:
         """skv_pages_scatter: the way back, from decode()'s output into the sequence's pages; x as gather() takes it."""
         tokens = int(tokens)
-        if self._tokens(tokens, x):
-            self._keep(stream, x)
-            with self._made_on(stream):  # kept for the call by the order of its stream
-                x = x[:, :, :, :tokens].contiguous()
-        _check(self._lib.skv_pages_scatter(self._sh, self._pg, int(seq), int(first), tokens, x.data_ptr(),
-                                        self._st, self._call(stream, x)), "skv_pages_scatter")
+        if self._tokens(tokens, x, stream):
+            _check(self._lib.skv_pages_scatter(self._sh, self._pg, int(seq), int(first), tokens, x.data_ptr(),
+                                            self._st, self._call(stream, x)), "skv_pages_scatter")
 
     def attend(self, layer: int, q, seqs, scale=None, k_scale=None, v_scale=None, out=None, lse=None, stream=None):
         """skv_attend: attention of q [n][q_heads][head_dim], one token of each sequence in seqs, over the cached
