@@ -420,6 +420,8 @@ class Pages:
         """The tensors' memory, and the cache's own, goes to no other tensor before the stream has done with it.  An
         external stream may be gone by the time that a tensor is freed, and is not named to the allocator."""
         if isinstance(stream, torch.cuda.Stream) and not isinstance(stream, torch.cuda.ExternalStream):
+            if _raw_stream is not None and stream.cuda_stream == _raw_stream(self._index):
+                return  # the current one
             if stream.cuda_stream not in self._streams:
                 self._streams.add(stream.cuda_stream)
                 given += (self.pool, self.table, self.lens, self.refs, self.workspace, self.attend_workspace, self.status)
